@@ -376,6 +376,90 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
                          const float *h0, void *outputs, void *final_state, ss_stream_t stream);
 
 /*
+ * Gated delta rule, prompt scan.  Per batch row and value head h (which reads the query
+ * and key head h / (heads_v / heads_k)), with a dk x dv state in fp32:
+ *
+ *   a_t = exp(g[b,t,h])                 (0 where reset[b,t] != 0: the state is discarded)
+ *   u_t = beta[b,t,h] * (v_t - a_t * S_{t-1}^T k_t)
+ *   S_t = a_t * S_{t-1} + k_t u_t^T
+ *   outputs[b,t,h,:] = scale * S_t^T q_t
+ *
+ * from S_{-1} = h0[b,h] (zeros when NULL) to final_state[b,h] = S_{seq-1}.  Beside
+ * ss_gated_scan (which adds k_t v_t^T as it comes) the write first takes away what the
+ * key reads already.
+ *
+ *   q, k        : [batch, seq, heads_k, dk] dtype   consecutive tokens q_stride, k_stride
+ *   v           : [batch, seq, heads_v, dv] dtype   and v_stride elements apart (at least
+ *                 the heads' width; batch rows seq * stride apart), so that all three may
+ *                 be slices of one projection's output
+ *   g           : [batch, seq, heads_v] float32, nullable (no decay): log decays, any
+ *                 value below +infinity; -infinity discards the state
+ *   beta        : [batch, seq, heads_v] float32, nullable (1), any value
+ *   reset       : [batch, seq] uint8, nullable
+ *   h0          : [batch, heads_v, dk, dv] float32, nullable
+ *   flags       : SS_QK_L2NORM: q and k stand for q / sqrt(|q|^2 + 1e-6) and the same of k
+ *   outputs     : [batch, seq, heads_v, dv] dtype
+ *   final_state : [batch, heads_v, dk, dv] float32, nullable; may be h0 itself
+ *   workspace   : device buffer of at least ss_delta_workspace_bytes() bytes, 16-byte
+ *                 aligned, or NULL.  Its contents need no preparation and mean nothing
+ *                 between calls; calls that share it must be ordered.  Without it (or for
+ *                 shapes that need none) the token-by-token kernel runs.
+ *
+ * heads_v must be a multiple of heads_k (SS_ERR_SHAPE), dk at most 256
+ * (SS_ERR_UNSUPPORTED).  Inputs must be finite (but for g) where they are read.
+ */
+enum { SS_QK_L2NORM = 4u };
+SS_API int ss_delta_scan(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,
+                         ss_dtype_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const float *g, const float *beta,
+                         const uint8_t *reset, const float *h0, float scale, uint32_t flags, void *outputs,
+                         float *final_state, void *workspace, size_t workspace_bytes, ss_stream_t stream);
+
+/* Workspace bytes ss_delta_scan uses for this shape (0: none, or an invalid shape). */
+SS_API int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk,
+                                        int64_t dv, ss_dtype_t dtype);
+
+/*
+ * Gated delta rule, decode step: one token of the recurrence of ss_delta_scan for every
+ * (batch row, value head), updating `state` in place.
+ *
+ *   state   : [batch, heads_v, dk, dv] float32 (in/out)
+ *   q, k    : [batch, heads_k, dk] dtype, batch rows q_stride, k_stride elements apart
+ *   v       : [batch, heads_v, dv] dtype, batch rows v_stride elements apart
+ *   g, beta : [batch, heads_v] float32, nullable (no decay; 1)
+ *   y       : [batch, heads_v, dv] dtype (output)
+ * scale, flags and the limits are those of ss_delta_scan.
+ */
+SS_API int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,
+                           float *state, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, const float *g, const float *beta, float scale,
+                           uint32_t flags, void *y, ss_stream_t stream);
+
+/*
+ * Group norm of each row's channels, with an activation or a gate: what a state-space
+ * layer applies to its heads before the output projection (rows are tokens; the
+ * statistics never mix tokens).  Per row and group of `size` consecutive channels:
+ *
+ *   x' = x silu(gate)  with SS_NORM_GATE_FIRST and a gate, x otherwise
+ *   n  = (x' - m) / sqrt(mean((x' - m)^2) + eps),  m = mean(x') with SS_NORM_CENTER, else 0
+ *   n  = n * weight + bias;  n = silu(n) with SS_NORM_SILU
+ *   y  = n silu(gate)  with a gate and without SS_NORM_GATE_FIRST, n otherwise
+ *
+ *   x, gate      : [rows, groups * size] dtype, rows x_stride, gate_stride elements apart
+ *                  (gate nullable)
+ *   weight, bias : [groups * size] float32, or [size] (every group's) with SS_NORM_SHARED;
+ *                  each nullable (1, 0)
+ *   y            : [rows, groups * size] dtype (output, contiguous)
+ *
+ * size at most SS_GROUP_NORM_MAX_SIZE and eps >= 0 (SS_ERR_UNSUPPORTED otherwise).
+ */
+#define SS_GROUP_NORM_MAX_SIZE 16384
+enum { SS_NORM_CENTER = 1u, SS_NORM_GATE_FIRST = 2u, SS_NORM_SILU = 4u, SS_NORM_SHARED = 8u };
+SS_API int ss_group_norm(int64_t rows, int64_t groups, int64_t size, ss_dtype_t dtype, const void *x,
+                         int64_t x_stride, const void *gate, int64_t gate_stride, const float *weight,
+                         const float *bias, float eps, uint32_t flags, void *y, ss_stream_t stream);
+
+/*
  * Sequence cut into segments (one per GPU, say) -- the two joining steps.
  *
  * The scan's recurrence composes associatively ("s6_reset" blog draft, Associative

@@ -59,6 +59,9 @@ def _load():
             lib.ss_oracle_conv_silu.restype = ctypes.c_int
             lib.ss_oracle_gated_scan.argtypes = [_i64, _i64, _i64, _i64] + [_dp] * 7 + [ctypes.c_int]
             lib.ss_oracle_gated_scan.restype = ctypes.c_int
+            lib.ss_oracle_delta_scan.argtypes = [_i64] * 6 + [_dp] * 5 + [_u8p, _dp, ctypes.c_double, ctypes.c_int,
+                                                                           _dp, _dp, ctypes.c_int]
+            lib.ss_oracle_delta_scan.restype = ctypes.c_int
             lib.ss_oracle_segment.argtypes = [_i64, _i64, _i64, _i64] + [_dp] * 5 + [
                 _u8p, ctypes.c_int, _dp, _dp, ctypes.c_int]
             lib.ss_oracle_segment.restype = ctypes.c_int
@@ -217,6 +220,59 @@ def gated_scan(q, k, v, gamma, h0=None, *, nthreads=None):
                                       _ptr(y), _ptr(fs), int(nthreads or num_threads()))
     _check(rc, "ss_oracle_gated_scan")
     return {"outputs": y, "final_state": fs}
+
+
+def delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None, qk_l2norm=False, nthreads=None):
+    """Gated delta rule oracle: S_t = a_t S_{t-1} + k_t u_t^T, u_t = beta_t (v_t - a_t
+    S_{t-1}^T k_t), y_t = scale S_t^T q_t, a_t = exp(g_t), 0 at a reset.  q, k [B, S, Hk,
+    Dk]; v [B, S, Hv, Dv]; g, beta [B, S, Hv] or None; reset [B, S]; h0 [B, Hv, Dk, Dv].
+    A decode step is the call with S = 1.  Returns dict(outputs, final_state)."""
+    q, k, v, g, beta, h0 = (_f64(a) for a in (q, k, v, g, beta, h0))
+    reset = _u8(reset)
+    bt, sl, hk, dk = q.shape
+    hv, dv = v.shape[2:]
+    if k.shape != q.shape or v.shape[:2] != (bt, sl):
+        raise ValueError("inconsistent shapes")
+    for a in (g, beta):
+        if a is not None and a.shape != (bt, sl, hv):
+            raise ValueError("g and beta must be [B, S, Hv]")
+    if reset is not None and reset.shape != (bt, sl):
+        raise ValueError("reset must be [B, S]")
+    if h0 is not None and h0.shape != (bt, hv, dk, dv):
+        raise ValueError("h0 must be [B, Hv, Dk, Dv]")
+    y = np.empty((bt, sl, hv, dv))
+    fs = np.empty((bt, hv, dk, dv))
+    rc = _load().ss_oracle_delta_scan(bt, sl, hk, hv, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                      _ptr(reset, _u8p), _ptr(h0), dk ** -0.5 if scale is None else float(scale),
+                                      int(bool(qk_l2norm)), _ptr(y), _ptr(fs), int(nthreads or num_threads()))
+    _check(rc, "ss_oracle_delta_scan")
+    return {"outputs": y, "final_state": fs}
+
+
+def group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=False, center=True, activation=None,
+               eps=1e-5):
+    """Group norm over the last dimension in float64 (numpy): per row and group,
+    (x - mean) / sqrt(var + eps), times weight plus bias, SiLU, times silu(gate)."""
+    x, weight, bias, gate = (_f64(a) for a in (x, weight, bias, gate))
+
+    def silu(a):
+        return a / (1.0 + np.exp(-a))
+
+    shape = x.shape
+    if gate is not None and gate_first:
+        x = x * silu(gate)
+    x = x.reshape(-1, groups, shape[-1] // groups)
+    if center:
+        x = x - x.mean(-1, keepdims=True)
+    x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    for a, mul in ((weight, True), (bias, False)):
+        if a is not None:
+            a = a.reshape((1, -1, x.shape[-1]))
+            x = x * a if mul else x + a
+    if activation == "silu":
+        x = silu(x)
+    x = x.reshape(shape)
+    return x * silu(gate) if gate is not None and not gate_first else x
 
 
 def segment(x, dt, A, B, dt_bias=None, reset=None, *, dt_softplus=True, nthreads=None):

@@ -441,3 +441,82 @@ int ss_oracle_conv_silu(int64_t batch, int64_t channels, int64_t seq, int64_t K,
     (void)nthreads;
     return ORC_OK;
 }
+
+/*
+ * Gated delta rule: per batch item b and value head h (key head h / (hv / hk)),
+ *
+ *   a_t = reset[b,t] ? 0 : exp(g[b,t,h])
+ *   u_t = beta[b,t,h] (v_t - a_t S_{t-1}^T k_t)
+ *   S_t = a_t S_{t-1} + k_t u_t^T,   y_t = scale S_t^T q_t
+ *
+ * with q and k divided by sqrt(|.|^2 + 1e-6) when l2norm.  Layouts: q, k [batch, seq,
+ * hk, dk]; v, y [batch, seq, hv, dv]; g, beta [batch, seq, hv] (g NULL: 0, beta NULL: 1);
+ * reset [batch, seq] (nullable); h0 (nullable), final_state [batch, hv, dk, dv].  The
+ * token loop in sequence order; OpenMP over (batch item, head) only.
+ */
+int ss_oracle_delta_scan(int64_t batch, int64_t seq, int64_t hk, int64_t hv, int64_t dk, int64_t dv,
+                         const double *q, const double *k, const double *v, const double *g,
+                         const double *beta, const uint8_t *reset, const double *h0, double scale,
+                         int l2norm, double *y, double *final_state, int nthreads)
+{
+    if (!q || !k || !v || !y || !final_state)
+        return ORC_ERR_NULL;
+    if (batch <= 0 || seq <= 0 || hk <= 0 || hv <= 0 || dk <= 0 || dv <= 0 || hv % hk)
+        return ORC_ERR_SHAPE;
+    int failed = 0;
+#ifdef _OPENMP
+#pragma omp parallel for num_threads(nthreads > 0 ? nthreads : 1) schedule(static)
+#endif
+    for (int64_t bh = 0; bh < batch * hv; ++bh) {
+        const int64_t b = bh / hv, h = bh % hv, hq = h / (hv / hk);
+        double *S = (double *)malloc(sizeof(double) * (size_t)(dk * dv + dv + 2 * dk));
+        if (!S) {
+            failed = 1;
+            continue;
+        }
+        double *u = S + dk * dv, *kn = u + dv, *qn = kn + dk;
+        for (int64_t i = 0; i < dk * dv; ++i)
+            S[i] = h0 ? h0[bh * dk * dv + i] : 0.0;
+        for (int64_t t = 0; t < seq; ++t) {
+            const int64_t tok = b * seq + t;
+            const double *kt = k + (tok * hk + hq) * dk, *qt = q + (tok * hk + hq) * dk;
+            const double *vt = v + (tok * hv + h) * dv;
+            const double be = beta ? beta[tok * hv + h] : 1.0;
+            double kk = 0.0, qq = 0.0;
+            for (int64_t i = 0; i < dk; ++i) {
+                kk += kt[i] * kt[i];
+                qq += qt[i] * qt[i];
+            }
+            for (int64_t i = 0; i < dk; ++i) {
+                kn[i] = l2norm ? kt[i] / sqrt(kk + 1e-6) : kt[i];
+                qn[i] = l2norm ? qt[i] / sqrt(qq + 1e-6) : qt[i];
+            }
+            const int cut = reset && reset[tok];
+            const double a = cut ? 0.0 : (g ? exp(g[tok * hv + h]) : 1.0);
+            for (int64_t j = 0; j < dv; ++j)
+                u[j] = 0.0;
+            for (int64_t i = 0; i < dk; ++i)
+                for (int64_t j = 0; j < dv; ++j) {
+                    S[i * dv + j] *= a;
+                    u[j] += S[i * dv + j] * kn[i];
+                }
+            for (int64_t j = 0; j < dv; ++j)
+                u[j] = be * (vt[j] - u[j]);
+            double *yt = y + (tok * hv + h) * dv;
+            for (int64_t j = 0; j < dv; ++j)
+                yt[j] = 0.0;
+            for (int64_t i = 0; i < dk; ++i)
+                for (int64_t j = 0; j < dv; ++j) {
+                    S[i * dv + j] += kn[i] * u[j];
+                    yt[j] += S[i * dv + j] * qn[i];
+                }
+            for (int64_t j = 0; j < dv; ++j)
+                yt[j] *= scale;
+        }
+        for (int64_t i = 0; i < dk * dv; ++i)
+            final_state[bh * dk * dv + i] = S[i];
+        free(S);
+    }
+    (void)nthreads;
+    return failed ? ORC_ERR_NOMEM : ORC_OK;
+}

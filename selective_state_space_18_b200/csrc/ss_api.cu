@@ -15,10 +15,12 @@
 #include "ss_gated_scan.cuh"
 #include "ss_gated_tc.cuh"
 #include "ss_segment.cuh"
+#include "ss_delta.cuh"
+#include "ss_group_norm.cuh"
 
 namespace {
 
-constexpr int kAbiMajor = 3, kAbiMinor = 0;
+constexpr int kAbiMajor = 3, kAbiMinor = 1;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -1379,3 +1381,5 @@ int ss_join_segments(int64_t segments, int64_t count, const float *composites, i
 }
 
 } // extern "C"
+
+#include "ss_delta_api.cuh"

@@ -1,0 +1,295 @@
+// ss_delta_api.cuh -- host side of the gated delta rule and the group norm: validation,
+// dispatch and launch.  Included by ss_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// Elements from the first to one past the last of `rows` rows of `n` elements, `stride`
+// apart; false when that does not fit.
+bool row_extent(int64_t rows, int64_t stride, int64_t n, int64_t *out)
+{
+    int64_t m = 0;
+    return stride >= n && mul_ok(rows, stride, &m) && m < INT64_MAX / 8 && ((*out = m - stride + n), true);
+}
+
+struct DeltaSizes { // element counts of one call's buffers
+    int64_t qn, kn, vn, gates, rows, yn, states;
+};
+
+// Everything the two entry points check alike.  rows: batch * seq (prompt) or batch.
+int delta_check(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,
+                const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                const float *g, const float *beta, uint32_t flags, DeltaSizes *z)
+{
+    if (batch <= 0 || seq <= 0 || heads_k <= 0 || heads_v <= 0 || dk <= 0 || dv <= 0)
+        return SS_ERR_SHAPE;
+    if (dtype != SS_F32 && dtype != SS_BF16)
+        return SS_ERR_DTYPE;
+    if (dk > 256 || (flags & ~uint32_t(SS_QK_L2NORM)))
+        return SS_ERR_UNSUPPORTED;
+    if (heads_v % heads_k != 0 || heads_v > (1 << 20) || dv > (1 << 20))
+        return SS_ERR_SHAPE;
+    int64_t sh = 0, sd = 0;
+    if (!mul_ok(batch, seq, &z->rows) || !mul_ok(z->rows, heads_v, &z->gates) || !mul_ok(z->gates, dv, &z->yn) ||
+        !mul_ok(batch, heads_v, &sh) || !mul_ok(sh, dk * dv, &sd) || z->yn > INT64_MAX / 8 || sd > INT64_MAX / 8)
+        return SS_ERR_SHAPE;
+    z->states = sd;
+    if (!row_extent(z->rows, q_stride, heads_k * dk, &z->qn) || !row_extent(z->rows, k_stride, heads_k * dk, &z->kn) ||
+        !row_extent(z->rows, v_stride, heads_v * dv, &z->vn))
+        return SS_ERR_SHAPE;
+    const size_t es = dtype == SS_BF16 ? 2 : 4;
+    if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(g, 4) || !aligned(beta, 4))
+        return SS_ERR_ALIGN;
+    return SS_OK;
+}
+
+template <typename T, int R4> int launch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
+{
+    static std::atomic<uint64_t> smem_done{0};
+    constexpr size_t kSmem = ss::DeltaRecSmem<R4>::kBytes;
+    const int st = ensure_smem(ss::ss_delta_rec_kernel<T, R4>, kSmem, smem_done);
+    if (st != SS_OK)
+        return st;
+    const int64_t tiles = (a.dv + ss::kDrCols - 1) / ss::kDrCols;
+    int64_t grid = 0;
+    if (!mul_ok(a.batch * a.heads_v, tiles, &grid) || grid > 0x7fffffffLL)
+        return SS_ERR_SHAPE;
+    ss::ss_delta_rec_kernel<T, R4><<<unsigned(grid), ss::kDrThreads, kSmem, s>>>(a);
+    return launch_status();
+}
+
+template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
+{
+    if (a.dk <= 32)
+        return launch_delta_rec<T, 1>(a, s);
+    if (a.dk <= 64)
+        return launch_delta_rec<T, 2>(a, s);
+    return a.dk <= 128 ? launch_delta_rec<T, 4>(a, s) : launch_delta_rec<T, 8>(a, s);
+}
+
+template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cudaStream_t s)
+{
+    a.col_tiles = (a.dv + ss::kDuCols - 1) / ss::kDuCols;
+    int64_t grid = 0;
+    if (!mul_ok(a.batch * a.heads_v, a.col_tiles, &grid) || grid > 0x7fffffffLL)
+        return SS_ERR_SHAPE;
+    if (a.dv % 4 == 0 && aligned(a.state, 16))
+        ss::ss_delta_update_kernel<T, J, true><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
+    else
+        ss::ss_delta_update_kernel<T, J, false><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
+    return launch_status();
+}
+
+template <typename T> int dispatch_delta_update(const ss::DeltaUpdateArgs &a, cudaStream_t s)
+{
+    if (a.dk <= 64)
+        return launch_delta_update<T, 4>(a, s);
+    return a.dk <= 128 ? launch_delta_update<T, 8>(a, s) : launch_delta_update<T, 16>(a, s);
+}
+
+template <typename T, int VEC, int NV, bool CTA> int launch_group_norm(const ss::GroupNormArgs &a, cudaStream_t s)
+{
+    int sms = 0;
+    if (device_sm_count(&sms) != SS_OK)
+        return SS_ERR_CUDA;
+    const int64_t per_cta = CTA ? 1 : ss::kGnThreads >> a.team_log2;
+    const int64_t blocks = (a.rows * a.groups + per_cta - 1) / per_cta;
+    const int64_t most = int64_t(sms) * 32;
+    ss::ss_group_norm_kernel<T, VEC, NV, CTA>
+        <<<unsigned(blocks < most ? blocks : most), ss::kGnThreads, 0, s>>>(a);
+    return launch_status();
+}
+
+// Teams: the fewest lanes of a warp that hold a group in one vector each; up to eight
+// vectors a lane for a whole warp; beyond that the CTA.
+template <typename T, int VEC> int dispatch_group_norm(ss::GroupNormArgs &a, cudaStream_t s)
+{
+    const int vecs = (a.size + VEC - 1) / VEC;
+    a.team_log2 = 0;
+    while (a.team_log2 < 5 && (1 << a.team_log2) < vecs)
+        ++a.team_log2;
+    if (vecs <= 32)
+        return launch_group_norm<T, VEC, 1, false>(a, s);
+    if (vecs <= 64)
+        return launch_group_norm<T, VEC, 2, false>(a, s);
+    if (vecs <= 128)
+        return launch_group_norm<T, VEC, 4, false>(a, s);
+    if (vecs <= 256)
+        return launch_group_norm<T, VEC, 8, false>(a, s);
+    if (vecs <= 4 * ss::kGnThreads)
+        return launch_group_norm<T, VEC, 4, true>(a, s);
+    if constexpr (VEC == 1) {
+        if (vecs > 16 * ss::kGnThreads)
+            return launch_group_norm<T, VEC, 64, true>(a, s);
+    }
+    return launch_group_norm<T, VEC, VEC == 8 ? 8 : 16, true>(a, s);
+}
+
+} // namespace
+
+extern "C" {
+
+int ss_delta_scan(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,
+                  ss_dtype_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                  int64_t v_stride, const float *g, const float *beta, const uint8_t *reset, const float *h0,
+                  float scale, uint32_t flags, void *outputs, float *final_state, void *workspace,
+                  size_t workspace_bytes, ss_stream_t stream)
+{
+    if (!q || !k || !v || !outputs)
+        return SS_ERR_NULL;
+    DeltaSizes z{};
+    const int st = delta_check(batch, seq, heads_k, heads_v, dk, dv, dtype, q, q_stride, k, k_stride, v, v_stride, g,
+                               beta, flags, &z);
+    if (st != SS_OK)
+        return st;
+    const size_t es = dtype == SS_BF16 ? 2 : 4;
+    if (!aligned(outputs, es) || !aligned(h0, 4) || !aligned(final_state, 4) || !aligned(workspace, 16))
+        return SS_ERR_ALIGN;
+    if (workspace && int64_t(workspace_bytes) < ss_delta_workspace_bytes(batch, seq, heads_k, heads_v, dk, dv, dtype))
+        return SS_ERR_WORKSPACE;
+    const size_t ybytes = size_t(z.yn) * es, sbytes = size_t(z.states) * 4;
+    const void *in_p[] = {q, k, v, g, beta, reset, h0};
+    const size_t in_n[] = {size_t(z.qn) * es, size_t(z.kn) * es, size_t(z.vn) * es, size_t(z.gates) * 4,
+                           size_t(z.gates) * 4, size_t(z.rows), sbytes};
+    const void *out_p[] = {outputs, final_state, workspace};
+    const size_t out_n[] = {ybytes, sbytes, workspace_bytes};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 7; ++i) {
+            if (o == 1 && i == 6 && final_state == h0)
+                continue; // chaining in place
+            if (overlaps(out_p[o], out_n[o], in_p[i], in_n[i]))
+                return SS_ERR_ALIAS;
+        }
+        for (int i = 0; i < o; ++i)
+            if (overlaps(out_p[o], out_n[o], out_p[i], out_n[i]))
+                return SS_ERR_ALIAS;
+    }
+    ss::DeltaArgs a{};
+    a.batch = batch;
+    a.seq = seq;
+    a.heads_k = int(heads_k);
+    a.heads_v = int(heads_v);
+    a.ratio = int(heads_v / heads_k);
+    a.dk = int(dk);
+    a.dv = int(dv);
+    a.q = q; a.k = k; a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.g = g;
+    a.beta = beta;
+    a.reset = reset;
+    a.h0 = h0;
+    a.y = outputs;
+    a.final_state = final_state;
+    a.scale = scale;
+    a.l2norm = (flags & SS_QK_L2NORM) ? 1 : 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == SS_BF16 ? dispatch_delta_rec<__nv_bfloat16>(a, s) : dispatch_delta_rec<float>(a, s);
+}
+
+int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,
+                                 ss_dtype_t dtype)
+{
+    (void)batch; (void)seq; (void)heads_k; (void)heads_v; (void)dk; (void)dv; (void)dtype;
+    return 0;
+}
+
+int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,
+                    float *state, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *g, const float *beta, float scale, uint32_t flags, void *y,
+                    ss_stream_t stream)
+{
+    if (!state || !q || !k || !v || !y)
+        return SS_ERR_NULL;
+    DeltaSizes z{};
+    const int st = delta_check(batch, 1, heads_k, heads_v, dk, dv, dtype, q, q_stride, k, k_stride, v, v_stride, g,
+                               beta, flags, &z);
+    if (st != SS_OK)
+        return st;
+    const size_t es = dtype == SS_BF16 ? 2 : 4;
+    if (!aligned(y, es) || !aligned(state, 4))
+        return SS_ERR_ALIGN;
+    const size_t ybytes = size_t(z.yn) * es, sbytes = size_t(z.states) * 4;
+    const void *in_p[] = {q, k, v, g, beta};
+    const size_t in_n[] = {size_t(z.qn) * es, size_t(z.kn) * es, size_t(z.vn) * es, size_t(z.gates) * 4,
+                           size_t(z.gates) * 4};
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(y, ybytes, in_p[i], in_n[i]) || overlaps(state, sbytes, in_p[i], in_n[i]))
+            return SS_ERR_ALIAS;
+    if (overlaps(y, ybytes, state, sbytes))
+        return SS_ERR_ALIAS;
+    ss::DeltaUpdateArgs a{};
+    a.batch = batch;
+    a.heads_k = int(heads_k);
+    a.heads_v = int(heads_v);
+    a.ratio = int(heads_v / heads_k);
+    a.dk = int(dk);
+    a.dv = int(dv);
+    a.state = state;
+    a.q = q; a.k = k; a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.g = g;
+    a.beta = beta;
+    a.y = y;
+    a.scale = scale;
+    a.l2norm = (flags & SS_QK_L2NORM) ? 1 : 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == SS_BF16 ? dispatch_delta_update<__nv_bfloat16>(a, s) : dispatch_delta_update<float>(a, s);
+}
+
+int ss_group_norm(int64_t rows, int64_t groups, int64_t size, ss_dtype_t dtype, const void *x, int64_t x_stride,
+                  const void *gate, int64_t gate_stride, const float *weight, const float *bias, float eps,
+                  uint32_t flags, void *y, ss_stream_t stream)
+{
+    if (!x || !y)
+        return SS_ERR_NULL;
+    if (rows <= 0 || groups <= 0 || size <= 0)
+        return SS_ERR_SHAPE;
+    if (dtype != SS_F32 && dtype != SS_BF16)
+        return SS_ERR_DTYPE;
+    if (size > SS_GROUP_NORM_MAX_SIZE ||
+        (flags & ~uint32_t(SS_NORM_CENTER | SS_NORM_GATE_FIRST | SS_NORM_SILU | SS_NORM_SHARED)))
+        return SS_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f))
+        return SS_ERR_UNSUPPORTED;
+    int64_t ch = 0, yn = 0, xn = 0, zn = 0, items = 0;
+    if (!mul_ok(groups, size, &ch) || ch > 0x7fffffffLL || !mul_ok(rows, groups, &items) || !mul_ok(rows, ch, &yn) ||
+        yn > INT64_MAX / 8 || !row_extent(rows, x_stride, ch, &xn) || (gate && !row_extent(rows, gate_stride, ch, &zn)))
+        return SS_ERR_SHAPE;
+    const size_t es = dtype == SS_BF16 ? 2 : 4;
+    if (!aligned(x, es) || !aligned(gate, es) || !aligned(y, es) || !aligned(weight, 4) || !aligned(bias, 4))
+        return SS_ERR_ALIGN;
+    const size_t pn = size_t((flags & SS_NORM_SHARED) ? size : ch) * 4;
+    const void *in_p[] = {x, gate, weight, bias};
+    const size_t in_n[] = {size_t(xn) * es, size_t(zn) * es, pn, pn};
+    for (int i = 0; i < 4; ++i)
+        if (overlaps(y, size_t(yn) * es, in_p[i], in_n[i]))
+            return SS_ERR_ALIAS;
+    ss::GroupNormArgs a{};
+    a.rows = rows;
+    a.groups = int(groups);
+    a.size = int(size);
+    a.x = x;
+    a.gate = gate;
+    a.x_stride = x_stride;
+    a.gate_stride = gate_stride;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = y;
+    a.eps = eps;
+    a.inv_size = 1.0f / float(size);
+    a.mode = int(flags);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t per = 16 / int64_t(es);
+    const bool vec = size % per == 0 && aligned(x, 16) && x_stride % per == 0 && aligned(y, 16) &&
+                     (!gate || (aligned(gate, 16) && gate_stride % per == 0)) && aligned(weight, 16) &&
+                     aligned(bias, 16);
+    if (dtype == SS_BF16)
+        return vec ? dispatch_group_norm<__nv_bfloat16, 8>(a, s) : dispatch_group_norm<__nv_bfloat16, 1>(a, s);
+    return vec ? dispatch_group_norm<float, 4>(a, s) : dispatch_group_norm<float, 1>(a, s);
+}
+
+} // extern "C"

@@ -159,6 +159,24 @@ def make_gated_inputs(batch, seq, dk, dv, dtype="bf16", *, seed=0, h0=False):
     return out
 
 
+def make_delta_inputs(batch, seq, heads_k, heads_v, dk, dv, dtype="bf16", *, seed=0, h0=False, reset_mean_doc=None):
+    """Seeded gated-delta-rule inputs: q, k [B, S, Hk, Dk] and v [B, S, Hv, Dv] as SiLU of
+    normals in ``dtype``; log decays g = -A softplus(a + bias) with A in [1, 16] and steps
+    log-uniform in [1e-3, 1e-1]; beta = sigmoid of normals; resets at document starts."""
+    g = _gen(seed)
+    silu = torch.nn.functional.silu
+    q, k = (silu(torch.randn(batch, seq, heads_k, dk, generator=g)).to(DTYPES[dtype]) for _ in range(2))
+    v = silu(torch.randn(batch, seq, heads_v, dv, generator=g)).to(DTYPES[dtype])
+    A = 1 + 15 * torch.rand(heads_v, generator=g)
+    u = torch.exp(math.log(1e-3) + math.log(100.0) * torch.rand(heads_v, generator=g))
+    a = torch.randn(batch, seq, heads_v, generator=g)
+    out = {"q": q, "k": k, "v": v, "g": -A * torch.nn.functional.softplus(a + torch.log(torch.expm1(u))),
+           "beta": torch.sigmoid(torch.randn(batch, seq, heads_v, generator=g))}
+    out["h0"] = 0.3 * torch.randn(batch, heads_v, dk, dv, generator=g) if h0 else None
+    out["reset"] = torch.rand(batch, seq, generator=g) < 1.0 / reset_mean_doc if reset_mean_doc else None
+    return out
+
+
 def make_workload(name_or_workload, **overrides):
     """Inputs for a named workload (prompt scan or decode update)."""
     w = WORKLOADS[name_or_workload] if isinstance(name_or_workload, str) else name_or_workload

@@ -24,6 +24,8 @@ BOUNDS_LIB_PATH = os.path.join(_PKG, "libssscan_bounds.so")
 SS_F32, SS_BF16 = 0, 1
 SS_DT_SOFTPLUS = 1
 SS_SCRATCH_ZERO = 2
+SS_QK_L2NORM = 4
+SS_NORM_CENTER, SS_NORM_GATE_FIRST, SS_NORM_SILU, SS_NORM_SHARED = 1, 2, 4, 8
 SS_STATIC_SCRATCH_BYTES = 1 << 20
 STATUS = {0: "SS_OK", 1: "SS_ERR_NULL", 2: "SS_ERR_SHAPE", 3: "SS_ERR_DTYPE", 4: "SS_ERR_ALIGN",
           5: "SS_ERR_UNSUPPORTED", 6: "SS_ERR_CUDA", 7: "SS_ERR_TIMEOUT", 8: "SS_ERR_ALIAS",
@@ -34,7 +36,8 @@ EXPORTS = ("ss_scan_fwd", "ss_scan_workspace_bytes", "ss_scan_plan", "ss_scan_st
            "ss_debug_set_gated_path",
            "ss_status_string", "ss_abi_version", "ss_debug_mufu_probe", "ss_debug_bounds_status",
            "ss_scan_fwd_static_scratch", "ss_scan_fwd_states", "ss_gated_scan", "ss_scan_fwd_conv",
-           "ss_state_update_conv", "ss_segment_decay", "ss_join_segments")
+           "ss_state_update_conv", "ss_segment_decay", "ss_join_segments", "ss_delta_scan",
+           "ss_delta_workspace_bytes", "ss_delta_update", "ss_group_norm")
 ABI_MAJOR = 3
 
 _lock = threading.Lock()
@@ -116,6 +119,17 @@ def load_library(path: str = LIB_PATH):
             lib.ss_debug_bounds_status.restype = ctypes.c_int
             lib.ss_debug_status.argtypes = [_vp]
             lib.ss_debug_status.restype = ctypes.c_int
+            lib.ss_delta_scan.argtypes = [_i64] * 6 + [ctypes.c_int] + [_vp, _i64] * 3 + [_vp] * 4 + [
+                ctypes.c_float, ctypes.c_uint32] + [_vp] * 3 + [ctypes.c_size_t, _vp]
+            lib.ss_delta_scan.restype = ctypes.c_int
+            lib.ss_delta_workspace_bytes.argtypes = [_i64] * 6 + [ctypes.c_int]
+            lib.ss_delta_workspace_bytes.restype = _i64
+            lib.ss_delta_update.argtypes = [_i64] * 5 + [ctypes.c_int, _vp] + [_vp, _i64] * 3 + [_vp] * 2 + [
+                ctypes.c_float, ctypes.c_uint32, _vp, _vp]
+            lib.ss_delta_update.restype = ctypes.c_int
+            lib.ss_group_norm.argtypes = [_i64] * 3 + [ctypes.c_int] + [_vp, _i64] * 2 + [_vp] * 2 + [
+                ctypes.c_float, ctypes.c_uint32, _vp, _vp]
+            lib.ss_group_norm.restype = ctypes.c_int
             lib.ss_abi_version.argtypes = []
             lib.ss_abi_version.restype = ctypes.c_int
             if lib.ss_abi_version() >> 16 != ABI_MAJOR:
@@ -668,3 +682,216 @@ def ss_join_segments(composites, rank=None, *, carry=None, final_state=None, wan
     if st != 0:
         raise SSError("ss_join_segments", st)
     return carry, final_state
+
+
+def _on_launch_stream(fn):
+    """Run a wrapper with its first tensor's device current and, when ``stream`` is given,
+    on that stream: the copies, outputs and workspaces that the wrapper makes then belong
+    to the stream the kernels run on, so nothing of theirs is reused before they end."""
+    lead = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        dev = (args[0] if args else kwargs[lead]).device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
+        if stream is None:
+            if torch.cuda.current_device() == dev.index:
+                return fn(*args, **kwargs)
+            with torch.cuda.device(dev):
+                return fn(*args, **kwargs)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return wrapper
+
+
+def _rows_of(t, name, dev, dtype, shape):
+    """A tensor [..., heads, d] whose rows (all but the last two dimensions) the library
+    reads in place: (tensor, elements between rows).  A view that is not evenly strided
+    rows of packed heads is copied."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    width = shape[-2] * shape[-1]
+    if t.is_contiguous():
+        return t, width
+    st = t.stride()
+    if (st[-1] == 1 or shape[-1] == 1) and (st[-2] == shape[-1] or shape[-2] == 1):
+        if len(shape) == 3:
+            step = st[0] if shape[0] > 1 else width
+        elif shape[1] > 1:
+            step = st[1] if shape[0] == 1 or st[0] == shape[1] * st[1] else 0
+        else:
+            step = st[0] if shape[0] > 1 else width
+        if step >= width:
+            return t, step
+    return t.contiguous(), width
+
+
+def _gate(t, name, dev, shape):
+    return None if t is None else _prep(t, name, dev, torch.float32, shape)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _delta_sizes(fn, q, v, lead):
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"{fn}: q, k and v must have {lead + 2} dimensions")
+    hk, dk = q.shape[-2:]
+    hv, dv = v.shape[-2:]
+    if hk == 0 or hv % hk:
+        raise ValueError(f"{fn}: {hv} value heads are not a multiple of {hk} key heads")
+    return hk, hv, dk, dv
+
+
+@_on_launch_stream
+def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None, qk_l2norm=False, outputs=None,
+                  final_state=None, return_final_state=True, workspace=True):
+    """Gated delta rule over a prompt: S_t = e^g_t S_{t-1} + k_t u_t^T with u_t = beta_t
+    (v_t - e^g_t S_{t-1}^T k_t), outputs_t = scale S_t^T q_t.  q, k: [batch, seq, heads_k,
+    dk]; v: [batch, seq, heads_v, dv] (float32 or bfloat16, slices of one projection are
+    read in place); g (log decays), beta: [batch, seq, heads_v] float32 or None (no decay,
+    1); reset: [batch, seq] bool/uint8, the state is discarded before that token; h0:
+    [batch, heads_v, dk, dv] float32.  scale defaults to dk ** -0.5; qk_l2norm divides q
+    and k by their lengths.  Returns {"outputs": [batch, seq, heads_v, dv] in the dtype of
+    q, "final_state": [batch, heads_v, dk, dv] float32 (None when not returned)}.
+
+    workspace: True (allocated for the call), False (none: the token-by-token kernel) or a
+    uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself."""
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    hk, hv, dk, dv = _delta_sizes("ss_delta_scan", q, v, 2)
+    bt, L = q.shape[:2]
+    q, qs = _rows_of(q, "q", dev, dt, (bt, L, hk, dk))
+    k, ks = _rows_of(k, "k", dev, dt, (bt, L, hk, dk))
+    v, vs = _rows_of(v, "v", dev, dt, (bt, L, hv, dv))
+    g = _gate(g, "g", dev, (bt, L, hv))
+    beta = _gate(beta, "beta", dev, (bt, L, hv))
+    h0 = _gate(h0, "h0", dev, (bt, hv, dk, dv))
+    if reset is not None:
+        reset = _prep(reset, "reset", dev, None, (bt, L))
+        if reset.dtype == torch.bool:
+            reset = reset.view(torch.uint8)
+        elif reset.dtype != torch.uint8:
+            raise TypeError("reset must be bool or uint8")
+    if outputs is None:
+        outputs = torch.empty((bt, L, hv, dv), device=dev, dtype=dt)
+    else:
+        outputs = _out(outputs, "outputs", dev, dt, (bt, L, hv, dv))
+    if final_state is not None:
+        final_state = _out(final_state, "final_state", dev, torch.float32, (bt, hv, dk, dv))
+    elif return_final_state:
+        final_state = torch.empty((bt, hv, dk, dv), device=dev, dtype=torch.float32)
+    lib = load_library()
+    if workspace is True:
+        need = lib.ss_delta_workspace_bytes(bt, L, hk, hv, dk, dv, code)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
+    elif workspace is False:
+        workspace = None
+    elif workspace is not None and (workspace.device != dev or workspace.dtype != torch.uint8
+                                    or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    st = lib.ss_delta_scan(bt, L, hk, hv, dk, dv, code, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(g),
+                           _addr(beta), _addr(reset), _addr(h0), dk ** -0.5 if scale is None else float(scale),
+                           SS_QK_L2NORM if qk_l2norm else 0, outputs.data_ptr(), _addr(final_state), _addr(workspace),
+                           0 if workspace is None else workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise SSError("ss_delta_scan", st)
+    return {"outputs": outputs, "final_state": final_state}
+
+
+def ss_delta_workspace_bytes(batch, seq, heads_k, heads_v, dk, dv, dtype=torch.bfloat16):
+    """Bytes of workspace ss_delta_scan uses for this shape (0: none)."""
+    return int(load_library().ss_delta_workspace_bytes(batch, seq, heads_k, heads_v, dk, dv,
+                                                       SS_BF16 if dtype == torch.bfloat16 else SS_F32))
+
+
+@_on_launch_stream
+def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=False, y=None):
+    """Decode step of the gated delta rule: ``state`` [batch, heads_v, dk, dv] float32 is
+    updated in place by one token.  q, k: [batch, heads_k, dk]; v: [batch, heads_v, dv];
+    g, beta: [batch, heads_v] float32 or None.  Returns y [batch, heads_v, dv]."""
+    dev, dt = state.device, q.dtype
+    code = _dtype_code(q)
+    hk, hv, dk, dv = _delta_sizes("ss_delta_update", q, v, 1)
+    bt = q.shape[0]
+    if state.dtype != torch.float32 or state.shape != (bt, hv, dk, dv) or not state.is_contiguous():
+        raise ValueError(f"state must be a contiguous float32 tensor of shape {(bt, hv, dk, dv)} (updated in place)")
+    q, qs = _rows_of(q, "q", dev, dt, (bt, hk, dk))
+    k, ks = _rows_of(k, "k", dev, dt, (bt, hk, dk))
+    v, vs = _rows_of(v, "v", dev, dt, (bt, hv, dv))
+    g = _gate(g, "g", dev, (bt, hv))
+    beta = _gate(beta, "beta", dev, (bt, hv))
+    if y is None:
+        y = torch.empty((bt, hv, dv), device=dev, dtype=dt)
+    else:
+        y = _out(y, "y", dev, dt, (bt, hv, dv))
+    st = load_library().ss_delta_update(bt, hk, hv, dk, dv, code, state.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
+                                        v.data_ptr(), vs, _addr(g), _addr(beta),
+                                        dk ** -0.5 if scale is None else float(scale),
+                                        SS_QK_L2NORM if qk_l2norm else 0, y.data_ptr(),
+                                        torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise SSError("ss_delta_update", st)
+    return y
+
+
+@_on_launch_stream
+def ss_group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=False, center=True, activation=None,
+                  eps=1e-5, y=None):
+    """Group norm over the last dimension: per row and group of channels // groups
+    consecutive channels, (x - mean) / sqrt(var + eps) (without the mean when ``center``
+    is false), times ``weight`` plus ``bias``, then SiLU (activation="silu"), then times
+    silu(gate); with ``gate_first`` the gate multiplies x before the statistics instead.
+    x, gate, y: [..., channels] float32 or bfloat16; weight, bias: float32 [channels], or
+    [channels // groups] for one set shared by all groups (both alike)."""
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    if x.dim() < 1:
+        raise ValueError("x must have a channel dimension")
+    shape, ch = x.shape, x.shape[-1]
+    groups = int(groups)
+    if groups <= 0 or ch % groups:
+        raise ValueError(f"{ch} channels do not divide into {groups} groups")
+    size = ch // groups
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+
+    def rows(t, name):
+        if t.device != dev or t.dtype != dt or t.shape != shape:
+            raise ValueError(f"{name} must be a {dt} tensor of shape {tuple(shape)} on {dev}")
+        t = t.reshape(-1, ch)
+        if t.shape[0] <= 1:
+            return t.contiguous(), ch
+        if (t.stride(1) != 1 and ch > 1) or t.stride(0) < ch:
+            t = t.contiguous()
+        return t, t.stride(0)
+
+    params = [t for t in (weight, bias) if t is not None]
+    shared = bool(params) and params[0].shape == (size,) and groups > 1
+    for t in params:
+        if t.device != dev or t.dtype != torch.float32 or t.shape != ((size,) if shared else (ch,)):
+            raise ValueError(f"weight and bias must be float32 tensors of shape ({ch},) or both ({size},) on {dev}")
+    weight = None if weight is None else weight.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    x, xs = rows(x, "x")
+    gate, zs = rows(gate, "gate") if gate is not None else (None, 0)
+    if y is None:
+        y = torch.empty(shape, device=dev, dtype=dt)
+    else:
+        y = _out(y, "y", dev, dt, shape)
+    flags = ((SS_NORM_CENTER if center else 0) | (SS_NORM_GATE_FIRST if gate_first else 0)
+             | (SS_NORM_SILU if activation else 0) | (SS_NORM_SHARED if shared else 0))
+    st = load_library().ss_group_norm(x.shape[0], groups, size, code, x.data_ptr(), xs, _addr(gate), zs, _addr(weight),
+                                      _addr(bias), float(eps), flags, y.data_ptr(),
+                                      torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise SSError("ss_group_norm", st)
+    return y
