@@ -16,6 +16,7 @@
 #include "ss_gated_tc.cuh"
 #include "ss_segment.cuh"
 #include "ss_delta.cuh"
+#include "ss_delta_tc.cuh"
 #include "ss_group_norm.cuh"
 
 namespace {

@@ -67,6 +67,88 @@ template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_
     return a.dk <= 128 ? launch_delta_rec<T, 4>(a, s) : launch_delta_rec<T, 8>(a, s);
 }
 
+// ---- the chunked form ----------------------------------------------------------------
+
+// Shapes the chunked form takes (bf16; q, k and v as rows of whole 16-byte vectors, which
+// TMA asks for).  Prompts of up to 16 tokens are walked token by token in less time than
+// the two launches take.
+bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_dtype_t dtype)
+{
+    return dtype == SS_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && seq > 16 && seq < (int64_t(1) << 31) - 64 &&
+           batch < (int64_t(1) << 31);
+}
+
+bool delta_chunked(const ss::DeltaArgs &a, const void *workspace)
+{
+    return workspace && delta_chunked_shape(a.batch, a.seq, a.dk, a.dv, SS_BF16) && aligned(a.q, 16) &&
+           aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.y, 16) && a.q_stride % 8 == 0 && a.k_stride % 8 == 0 && a.v_stride % 8 == 0 &&
+           a.q_stride * a.seq < (int64_t(1) << 38) && a.k_stride * a.seq < (int64_t(1) << 38) &&
+           a.v_stride * a.seq < (int64_t(1) << 38) &&
+           int64_t(a.heads_v) * a.dv * a.seq < (int64_t(1) << 38); // (byte strides of a tensor map end at 2^40)
+}
+
+// 4-D map (d, head, token, batch) over rows of heads, box (box_d, 1, 64 tokens, 1).
+bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, int64_t seq, int64_t batch,
+                  int64_t stride, uint32_t box_d, CUtensorMapSwizzle swizzle)
+{
+    PFN_cuTensorMapEncodeTiled enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(seq), cuuint64_t(batch)};
+    const cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(stride) * 2, cuuint64_t(stride) * 2 * cuuint64_t(seq)};
+    const cuuint32_t box[4] = {box_d, 1, uint32_t(ss::kDcChunk), 1}, estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s)
+{
+    static std::atomic<uint64_t> prep_done{0}, walk_done{0};
+    int st = ensure_smem(ss::ss_delta_prep_kernel, size_t(ss::DeltaPrepSmem::kBytes), prep_done);
+    if (st == SS_OK)
+        st = ensure_smem(ss::ss_delta_walk_kernel, size_t(ss::DwSmem::kBytes), walk_done);
+    if (st != SS_OK)
+        return st;
+    uint32_t *status = nullptr;
+    if (status_word_address(&status) != SS_OK)
+        return SS_ERR_CUDA;
+    ss::DeltaPrepArgs p{};
+    p.d = a;
+    p.nchunks = int((a.seq + ss::kDcChunk - 1) / ss::kDcChunk);
+    p.blocks = static_cast<unsigned char *>(workspace);
+    ss::DeltaWalkArgs w{};
+    w.batch = a.batch;
+    w.seq = a.seq;
+    w.heads_v = a.heads_v;
+    w.ratio = a.ratio;
+    w.dk = a.dk;
+    w.dv = a.dv;
+    w.nchunks = p.nchunks;
+    w.col_tiles = (a.dv + 127) / 128;
+    w.nks = (a.dk + 15) / 16;
+    w.blocks = p.blocks;
+    w.h0 = a.h0;
+    w.final_state = a.final_state;
+    int64_t units = 0, grid = 0;
+    if (!mul_ok(a.batch * a.heads_k, p.nchunks, &units) || units > 0x7fffffffLL ||
+        !mul_ok(a.batch * a.heads_v, w.col_tiles, &grid) || grid > 0x7fffffffLL)
+        return SS_ERR_SHAPE;
+    ss::DeltaWalkMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 128,
+                      CU_TENSOR_MAP_SWIZZLE_NONE))
+        return SS_ERR_CUDA;
+    ss::ss_delta_prep_kernel<<<unsigned(units), ss::kDpThreads, ss::DeltaPrepSmem::kBytes, s>>>(p);
+    if ((st = launch_status()) != SS_OK)
+        return st;
+    ss::ss_delta_walk_kernel<<<unsigned(grid), ss::kDwThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
+    return launch_status();
+}
+
 template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cudaStream_t s)
 {
     a.col_tiles = (a.dv + ss::kDuCols - 1) / ss::kDuCols;
@@ -185,14 +267,22 @@ int ss_delta_scan(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, 
     a.scale = scale;
     a.l2norm = (flags & SS_QK_L2NORM) ? 1 : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == SS_BF16 ? dispatch_delta_rec<__nv_bfloat16>(a, s) : dispatch_delta_rec<float>(a, s);
+    if (dtype == SS_F32)
+        return dispatch_delta_rec<float>(a, s);
+    return delta_chunked(a, workspace) ? launch_delta_chunked(a, workspace, s) : dispatch_delta_rec<__nv_bfloat16>(a, s);
 }
 
 int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,
                                  ss_dtype_t dtype)
 {
-    (void)batch; (void)seq; (void)heads_k; (void)heads_v; (void)dk; (void)dv; (void)dtype;
-    return 0;
+    if (batch <= 0 || seq <= 0 || heads_k <= 0 || heads_v <= 0 || dk <= 0 || dv <= 0 || heads_v % heads_k ||
+        !delta_chunked_shape(batch, seq, dk, dv, dtype))
+        return 0;
+    int64_t n = 0;
+    const int64_t chunks = (seq + ss::kDcChunk - 1) / ss::kDcChunk;
+    if (!mul_ok(batch, heads_v, &n) || !mul_ok(n, chunks, &n) || !mul_ok(n, ss::kDcBlockBytes, &n))
+        return 0;
+    return n;
 }
 
 int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,

@@ -1,0 +1,922 @@
+// ss_delta_tc.cuh -- the gated delta rule's prompt scan in chunked form on the tensor
+// cores: a kernel that prepares every chunk by itself, and a kernel that walks the chunks.
+//
+// With the entering state H [dk x dv] and, inside a chunk of 64 tokens (i, j = 0..63),
+//   D_ij = exp(g_{j+1} + ... + g_i)   (0 when a reset lies in j+1..i, or j > i)
+//   E_i  = the same from the chunk's start to i, F_j = D_63,j
+//   r_i, p_i = 1 / |k_i| and scale / |q_i|  (1 and scale without the norm)
+// the recurrence S_t = a_t S_{t-1} + k_t u_t^T, u_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+// unrolls to a triangular system for the writes u and three products:
+//   (I + A) U = diag(beta) (V - diag(c) K H),  A_ij = beta_i r_i r_j D_ij k_i.k_j (j < i),
+//                                              c_i = r_i E_i
+//   Y  = diag(s) Q H + P U,    s_i = p_i E_i, P_ij = p_i r_j D_ij q_i.k_j (j <= i)
+//   H' = E_63 H + K^T diag(w) U,               w_j = r_j F_j
+// The norms of q and k are factors of rows and columns, so q and k enter every product as
+// they are stored.
+//
+// The preparation (ss_delta_prep_kernel, one CTA per chunk and key head) needs no state:
+// K K^T and Q K^T, the decays, T = (I + A)^{-1} diag(beta) by substitution in fp32, and
+// per chunk and value head a 19 KB block of the workspace: T (split into a bf16 high part
+// and a bf16 remainder) and P (bf16) as operand tiles, c, w, s and E_63.
+//
+// The walk (ss_delta_walk_kernel, one CTA per head and 128 value columns) keeps H in fp32
+// registers, transposed: tensor-memory lane = value column.  Every product then takes its
+// left operand from tensor memory, where the element-wise steps leave it with no pass
+// through shared memory, and its right operand straight from the TMA tiles of k and q:
+//   KH^T [128 x 64]  = H^T K^T              R^T = V^T - KH^T diag(c)
+//   U^T  [128 x 64]  = R^T T^T              (only the blocks of T on and below the diagonal)
+//   Y^T  [128 x 64]  = H^T (sQ)^T + U^T P^T
+//   dH^T [128 x dk]  = (w o U)^T K          H = E_63 H + dH
+//
+// Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
+// state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
+// products summed in fp32, so the final state follows fp32 arithmetic to about 5e-6 of
+// its size.  On the way to the outputs, which are rounded to bf16 anyway, H, sQ, P and U
+// enter rounded to bf16 once each (output error 3e-3 of the norm in all, the rounding of
+// the output itself being 1.7e-3).
+//
+// Decays.  The cumulative log2 decays are kept as a part of multiples of 1/64, which sums
+// and differences exactly, and a remainder below 1/128 a token, so the decay between two
+// tokens is exact to 1e-7 however much the chunk decays in all.  A token whose decay is
+// zero in fp32 (a reset, -inf, below 2^-160) cuts: cut counts tell which pairs it parts.
+#pragma once
+
+#include <cuda.h>
+#include "ss_device.cuh"
+#include "ss_gated_tc.cuh" // tensor-memory and tcgen05 primitives
+#include "ss_state_update.cuh" // bulk_load
+#include "ss_sync.cuh"
+#include "ss_delta.cuh"
+
+namespace ss {
+
+constexpr int kDcChunk = 64; // tokens per chunk
+
+// A block: T hi, T lo, four arrays of 64 floats (c, w, s and E_63), then P.  A matrix is
+// four slices ks of 32-byte rows in the 32-byte swizzle: columns 16 ks .. 16 ks + 15, rows
+// 0..63 of the first two slices and 32..63 of the last two (the rest is above the diagonal
+// and 0).  Products with it accumulate into two halves of 32 tokens each, always with
+// N = 32: MMAs into one accumulator are only ordered among themselves when they have one
+// shape.
+constexpr int kDcMat = 6144;
+__host__ __device__ constexpr int dc_slice(int ks) { return ks < 2 ? 2048 * ks : 4096 + 1024 * (ks - 2); }
+constexpr int kDcThi = 0, kDcTlo = kDcMat, kDcC = 2 * kDcMat, kDcW = kDcC + 256, kDcS = kDcW + 256, kDcE = kDcS + 256,
+              kDcP = kDcE + 256;
+constexpr int kDcHead = kDcP;                     // the part loaded ahead of P
+constexpr int kDcBlockBytes = kDcP + kDcMat;      // workspace per chunk and value head
+static_assert(kDcHead % 1024 == 0 && kDcBlockBytes == 19456, "workspace block");
+
+// Byte offset of element (i, j) of a matrix in its slices (i >= 32 when j >= 32): the
+// 16-byte half of a 32-byte row is XORed with bit 2 of the row (address bit 4 with bit 7).
+__device__ __forceinline__ int dc_elem(int i, int j)
+{
+    const int r = i - (j & 32), o = (j & 15) * 2;
+    return dc_slice(j >> 4) + r * 32 + (o ^ ((r & 4) << 2));
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr));
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct DeltaPrepArgs {
+    DeltaArgs d;
+    int nchunks;
+    unsigned char *blocks; // [batch, heads_v, nchunks] blocks
+};
+
+// ---- preparation ---------------------------------------------------------------------
+//
+// 128 threads.  Warp w computes rows 16 w .. 16 w + 15 of K K^T and Q K^T with mma.sync
+// (64 x 64 products of a microsecond in all do not repay tensor-memory round trips), only
+// up to the diagonal, and keeps them in registers for all value heads of the key head.
+// Per value head it scales its rows of both by the decays and leaves A and P in shared
+// memory.  T is built from A in place: the inverses of the four 16 x 16 diagonal blocks by
+// substitution, one column a lane, then twice T21 = -T22 (A21 T11) for pairs of blocks in
+// packed fp32, with the intermediate product in the empty block above the diagonal.
+
+constexpr int kDpThreads = 128;
+constexpr int kDpRow = 136;  // elements between rows of the q and k tiles (272 bytes)
+constexpr int kDpARow = 68;  // floats between rows of A
+struct DeltaPrepSmem {       // A and P take the place of the q and k tiles
+    static constexpr int kK = 0, kQ = kDcChunk * kDpRow * 2;
+    static constexpr int kA = 0, kP = kDcChunk * kDpARow * 4;
+    static constexpr int kScal = 2 * kQ; // per token: Gh, Gl, cut count, r, p, beta (64 floats each)
+    static constexpr int kBytes = kScal + 6 * 256 + 16;
+    static_assert(kP + kDcMat <= kScal, "A and P inside the tiles");
+};
+
+// NR rows of 4 columns of a product: o[r][0..3] += sum_{k < K} a[(row r) k] b[k][0..3]; a
+// and b point into the A array.
+template <int NR> __device__ __forceinline__ void dp_rows(const float *const (&ar)[NR], const float *b, int K, float2 (&o)[NR][2])
+{
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+        o[r][0] = o[r][1] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < K; k += 4) {
+        float av[NR][4];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float4 v = *reinterpret_cast<const float4 *>(ar[r] + k);
+            av[r][0] = v.x, av[r][1] = v.y, av[r][2] = v.z, av[r][3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 v = *reinterpret_cast<const float4 *>(b + (k + e) * kDpARow);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float2 x = make_float2(av[r][e], av[r][e]);
+                o[r][0] = __ffma2_rn(x, make_float2(v.x, v.y), o[r][0]);
+                o[r][1] = __ffma2_rn(x, make_float2(v.z, v.w), o[r][1]);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const DeltaPrepArgs a)
+{
+    using Sm = DeltaPrepSmem;
+    extern __shared__ __align__(128) unsigned char dp_sm[];
+    const DeltaArgs &d = a.d;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = int(blockIdx.x % unsigned(d.heads_k));
+    const int64_t bc = blockIdx.x / unsigned(d.heads_k);
+    const int chunk = int(bc % a.nchunks);
+    const int64_t b = bc / a.nchunks;
+    const int64_t t0 = int64_t(chunk) * kDcChunk, tok0 = b * d.seq + t0;
+    const int n = int(d.seq - t0 < kDcChunk ? d.seq - t0 : kDcChunk); // tokens of this chunk
+    __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(dp_sm + Sm::kK);
+    __nv_bfloat16 *sq = reinterpret_cast<__nv_bfloat16 *>(dp_sm + Sm::kQ);
+    float *sA = reinterpret_cast<float *>(dp_sm + Sm::kA);
+    unsigned char *sPm = dp_sm + Sm::kP;
+    float *sGh = reinterpret_cast<float *>(dp_sm + Sm::kScal), *sGl = sGh + 64, *sR = sGh + 192, *sP = sGh + 256,
+          *sBeta = sGh + 320;
+    int *sN = reinterpret_cast<int *>(sGh + 128);
+    float *sRed = sGh + 384; // the first warp's totals
+
+    // q and k rows, zero beyond dk and beyond the sequence
+    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(d.k) + tok0 * d.k_stride + int64_t(hk) * d.dk;
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(d.q) + tok0 * d.q_stride + int64_t(hk) * d.dk;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = tid + kDpThreads * i, r = e >> 4, c = (e & 15) * 8;
+        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
+        if (r < n && c < d.dk) {
+            kv = __ldg(reinterpret_cast<const uint4 *>(kp + r * d.k_stride + c));
+            qv = __ldg(reinterpret_cast<const uint4 *>(qp + r * d.q_stride + c));
+        }
+        *reinterpret_cast<uint4 *>(sk + r * kDpRow + c) = kv;
+        *reinterpret_cast<uint4 *>(sq + r * kDpRow + c) = qv;
+    }
+    __syncthreads();
+    // lengths: thread t < 64 has k row t, the others q row t - 64
+    {
+        const __nv_bfloat16 *row = tid < 64 ? sk + tid * kDpRow : sq + (tid - 64) * kDpRow;
+        float2 s = make_float2(0.0f, 0.0f), s2 = s;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + 8 * c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+                (e & 1 ? s2 : s) = __ffma2_rn(x, x, e & 1 ? s2 : s);
+            }
+        }
+        const float inv = d.l2norm ? rsqrtf((s.x + s.y) + (s2.x + s2.y) + kDeltaEps) : 1.0f;
+        if (tid < 64)
+            sR[tid] = inv;
+        else
+            sP[tid - 64] = d.scale * inv;
+    }
+    // this warp's 16 rows of K K^T and Q K^T, columns 0 .. 16 warp + 15
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            kk[i][e] = qk[i][e] = 0.0f;
+    {
+        const uint32_t kb = smem_u32(sk), qb = smem_u32(sq);
+        // A fragments: rows 16 warp + lane % 16, columns 8 (lane / 16); B fragments (two
+        // n-tiles): token rows (lane % 8) + 8 (lane / 16), columns 8 ((lane / 8) % 2)
+        const uint32_t ao = uint32_t((16 * warp + (lane & 15)) * kDpRow + 8 * (lane >> 4)) * 2;
+        const uint32_t bo = uint32_t(((lane & 7) + 8 * (lane >> 4)) * kDpRow + 8 * ((lane >> 3) & 1)) * 2;
+        const int nks = (d.dk + 15) / 16;
+#pragma unroll 2
+        for (int ks = 0; ks < nks; ++ks) {
+            uint32_t ak[4], aq[4];
+            ldmatrix_x4(ak, kb + ao + 32 * ks);
+            ldmatrix_x4(aq, qb + ao + 32 * ks);
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                if (np <= warp) {
+                    uint32_t bk[4];
+                    ldmatrix_x4(bk, kb + bo + uint32_t(16 * np * kDpRow) * 2 + 32 * ks);
+                    mma_16816(kk[2 * np], ak, bk[0], bk[1]);
+                    mma_16816(kk[2 * np + 1], ak, bk[2], bk[3]);
+                    mma_16816(qk[2 * np], aq, bk[0], bk[1]);
+                    mma_16816(qk[2 * np + 1], aq, bk[2], bk[3]);
+                }
+            }
+        }
+    }
+    for (int hh = 0; hh < d.ratio; ++hh) {
+        const int h = hk * d.ratio + hh;
+        unsigned char *blk = a.blocks + ((b * d.heads_v + h) * a.nchunks + chunk) * kDcBlockBytes;
+        // ---- decays: thread t < 64 has token t -------------------------------------------
+        float gh = 0.0f, gl = 0.0f, be = 0.0f;
+        int cut = 0;
+        if (tid < 64) {
+            if (tid < n) {
+                const int64_t gi = (tok0 + tid) * d.heads_v + h;
+                be = d.beta ? __ldg(d.beta + gi) : 1.0f;
+                const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
+                if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
+                    cut = 1;
+                } else {
+                    gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
+                    gl = g2 - gh;
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float uh = __shfl_up_sync(0xffffffffu, gh, o), ul = __shfl_up_sync(0xffffffffu, gl, o);
+                const int uc = __shfl_up_sync(0xffffffffu, cut, o);
+                if (lane >= o) {
+                    gh += uh;
+                    gl += ul;
+                    cut += uc;
+                }
+            }
+            if (tid == 31) {
+                sRed[0] = gh;
+                sRed[1] = gl;
+                sRed[2] = __int_as_float(cut);
+            }
+        }
+        __syncthreads(); // the tiles, or the previous head's T and P, have been read too
+        if (tid < 64) {
+            if (tid >= 32) {
+                gh += sRed[0];
+                gl += sRed[1];
+                cut += __float_as_int(sRed[2]);
+            }
+            sGh[tid] = gh;
+            sGl[tid] = gl;
+            sN[tid] = cut;
+            sBeta[tid] = be;
+        }
+        __syncthreads();
+        if (tid < 64) {
+            const float e = cut ? 0.0f : ex2(gh + gl);
+            const float r = sR[tid];
+            reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
+            reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
+            reinterpret_cast<float *>(blk + kDcW)[tid] =
+                cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
+            reinterpret_cast<float *>(blk + kDcE)[tid] = sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
+        }
+        // ---- A and P ---------------------------------------------------------------------
+        {
+            const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
+            float gih[2], gil[2], bi[2], pi[2];
+            int ni[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = i0 + 8 * x;
+                gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
+                bi[x] = sBeta[i] * sR[i];
+                pi[x] = sP[i];
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                if (nt / 2 <= (warp | 1)) { // (above the diagonal: zeros of the slices of P)
+                    const int j = 8 * nt + j0;
+                    const float2 gjh = *reinterpret_cast<const float2 *>(sGh + j);
+                    const float2 gjl = *reinterpret_cast<const float2 *>(sGl + j);
+                    const int2 nj = *reinterpret_cast<const int2 *>(sN + j);
+                    const float2 rj = *reinterpret_cast<const float2 *>(sR + j);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int i = i0 + 8 * x;
+                        const float dx = j <= i && nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
+                        const float dy = j + 1 <= i && nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y))
+                                                                     : 0.0f;
+                        if (nt / 2 <= warp)
+                            *reinterpret_cast<float2 *>(sA + i * kDpARow + j) =
+                                make_float2(j < i ? bi[x] * dx * kk[nt][2 * x] : 0.0f,
+                                            j + 1 < i ? bi[x] * dy * kk[nt][2 * x + 1] : 0.0f);
+                        *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) =
+                            pack_bf16x2(pi[x] * dx * qk[nt][2 * x], pi[x] * dy * qk[nt][2 * x + 1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // ---- T -------------------------------------------------------------------------------
+        // the diagonal block of this warp: lane j solves (I + A) x = e_j (both half warps the
+        // same columns)
+        {
+            float *blkA = sA + 16 * warp * (kDpARow + 1);
+            float x[16];
+            const int j = lane & 15;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x[i] = i == j ? 1.0f : 0.0f;
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+                const float4 *row = reinterpret_cast<const float4 *>(blkA + i * kDpARow);
+#pragma unroll
+                for (int m = 0; m < (i + 3) / 4; ++m) { // A is 0 on and above the diagonal
+                    const float4 v = row[m];
+                    s0 = __ffma2_rn(make_float2(v.x, v.y), make_float2(x[4 * m], x[4 * m + 1]), s0);
+                    s1 = __ffma2_rn(make_float2(v.z, v.w), make_float2(x[4 * m + 2], x[4 * m + 3]), s1);
+                }
+                x[i] -= (s0.x + s0.y) + (s1.x + s1.y);
+            }
+            __syncwarp();
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    blkA[i * kDpARow + j] = x[i];
+            }
+        }
+        __syncthreads();
+        // pairs of 16 x 16 blocks: two warps each, one row of four columns a thread
+        {
+            float *base = sA + 32 * (warp >> 1) * (kDpARow + 1); // the pair's top left corner
+            const int i = (tid & 63) >> 2, c = 4 * (tid & 3);
+            float2 o[1][2];
+            const float *const a21[1] = {base + (16 + i) * kDpARow};
+            dp_rows<1>(a21, base + c, 16, o);
+            *reinterpret_cast<float4 *>(base + i * kDpARow + 16 + c) = make_float4(o[0][0].x, o[0][0].y, o[0][1].x, o[0][1].y);
+            __syncthreads();
+            const float *const t22[1] = {base + (16 + i) * kDpARow + 16};
+            dp_rows<1>(t22, base + 16 + c, 16, o);
+            *reinterpret_cast<float4 *>(base + (16 + i) * kDpARow + c) =
+                make_float4(-o[0][0].x, -o[0][0].y, -o[0][1].x, -o[0][1].y);
+        }
+        __syncthreads();
+        // the pair of 32 x 32 blocks: two rows of four columns a thread (the blocks above the
+        // diagonal 16 x 16 blocks hold leftovers and are skipped: T11's right half starts at
+        // row 16, T22's upper half ends at column 16)
+        {
+            const int right = warp >> 1; // A21 T11: the left or the right 16 columns
+            int i = (tid & 63) >> 2, c = 16 * right + 4 * (tid & 3);
+            float2 o[2][2];
+            const float *const a21[2] = {sA + (32 + i) * kDpARow + 16 * right, sA + (48 + i) * kDpARow + 16 * right};
+            dp_rows<2>(a21, sA + 16 * right * kDpARow + c, 32 - 16 * right, o);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float4 *>(sA + (i + 16 * r) * kDpARow + 32 + c) =
+                    make_float4(o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y);
+            __syncthreads();
+            const int low = warp >> 1; // T22 W: the upper or the lower 16 rows
+            i = 16 * low + 2 * ((tid & 63) >> 3);
+            c = 4 * (tid & 7);
+            const float *const t22[2] = {sA + (32 + i) * kDpARow + 32, sA + (33 + i) * kDpARow + 32};
+            dp_rows<2>(t22, sA + 32 + c, 16 + 16 * low, o);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float4 *>(sA + (32 + i + r) * kDpARow + c) =
+                    make_float4(-o[r][0].x, -o[r][0].y, -o[r][1].x, -o[r][1].y);
+        }
+        __syncthreads();
+        // ---- the block: T diag(beta) split, and P, in 16-byte pieces ----------------------
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            const int e = tid + kDpThreads * u; // piece: rows of 2, slices of 64, 64, 32, 32 rows
+            const int ks = e < 256 ? e >> 7 : 2 + ((e - 256) >> 6);
+            const int r = (e >> 1) & (e < 256 ? 63 : 31), i = r + (ks & 2) * 16, j = 16 * ks + 8 * (e & 1);
+            const int o = dc_elem(i, j);
+            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+            if (i >= 16 * ks) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float4 t = *reinterpret_cast<const float4 *>(sA + i * kDpARow + j + 4 * x);
+                    const float4 bj = *reinterpret_cast<const float4 *>(sBeta + j + 4 * x);
+                    split_bf16x2(t.x * bj.x, t.y * bj.y, hi[2 * x], lo[2 * x]);
+                    split_bf16x2(t.z * bj.z, t.w * bj.w, hi[2 * x + 1], lo[2 * x + 1]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(blk + kDcThi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(blk + kDcTlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(blk + kDcP + 16 * e) = *reinterpret_cast<const uint4 *>(sPm + 16 * e);
+        }
+    }
+}
+
+// ---- the walk ------------------------------------------------------------------------
+
+constexpr int kDwComputeWarps = 8;
+constexpr int kDwThreads = 32 * kDwComputeWarps + 32; // + the issuer warp
+constexpr uint32_t kDwTmemCols = 256;                 // two CTAs per SM
+// tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
+// 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
+// then R^T over it in the same form (16 columns per 16 tokens), then Y^T.  D2: U^T, then
+// (w o U)^T over it.
+constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192;
+
+struct DwSmem { // from a 1024-byte aligned base
+    static constexpr int kK = 0;                  // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
+    static constexpr int kQ = kK + 2 * 16384;     // q chunk, scaled in place: two tiles
+    static constexpr int kV = kQ + 16384;         // v chunk: [64 tokens x 128 values], not swizzled
+    static constexpr int kU = kV + 16384;         // U^T high parts [128 values x 64 tokens], then Y [64 x 128]
+    static constexpr int kB = kU + 16384;         // workspace blocks up to P: 2 stages
+    static constexpr int kP = kB + 2 * kDcHead;   // P
+    static constexpr int kBar = kP + kDcMat;
+    static constexpr int kTmem = kBar + 128;
+    static constexpr int kBytes = kBar + 256;
+};
+// two CTAs on an SM: 228 KB, 1 KB of it reserved for each
+static_assert(DwSmem::kBytes <= 113 * 1024, "shared memory of the walk");
+
+struct DeltaWalkArgs {
+    int64_t batch, seq;
+    int heads_v, ratio, dk, dv;
+    int nchunks, col_tiles, nks;  // nks: 16-key slices of the state
+    const unsigned char *blocks;
+    const float *h0;              // nullable
+    float *final_state;           // nullable
+};
+
+struct DeltaWalkMaps {
+    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), v and y (128, 1, 64, 1)
+};
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+                 : "memory");
+}
+// Matrix descriptor of K-major rows of 32 bytes in the 32-byte swizzle (layout type 6),
+// 8-row groups 256 bytes apart.
+__device__ __forceinline__ uint64_t sw32_desc(uint32_t saddr)
+{
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(6) << 61);
+}
+
+// A pair of values split into high parts and remainders, as split_bf16x2 does, with one
+// packed subtraction.
+__device__ __forceinline__ void dw_split2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 r = __ffma2_rn(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                                make_float2(-1.0f, -1.0f), x);
+    lo = pack_bf16x2(r.x, r.y);
+}
+
+__device__ __forceinline__ float2 dw_pair(const uint32_t (&r)[16], int e)
+{
+    return make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+}
+
+// One thread of a converged warp, chosen by the hardware: the compiler then knows that
+// one thread issues, and keeps the operands of tcgen05.mma in uniform registers.  (An MMA
+// of N = 64 takes 33 cycles so, and 48 when the thread is picked by its index; N = 32, 18
+// and 48.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Tile store, shared memory -> global, through a tensor map (what lies beyond the tensor
+// is left out).
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2,
+                                             int32_t c3)
+{
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
+                 : "memory");
+}
+// Barrier over the compute warps with an AND over every thread's predicate, so that after
+// a failed wait they leave the chunk loop together (a warp that left alone would strand
+// the others at the barrier).
+__device__ __forceinline__ bool dw_compute_sync_and(bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(uint32_t(v)), "n"(32 * kDwComputeWarps)
+                 : "memory");
+    return r != 0;
+}
+
+__global__ void __launch_bounds__(kDwThreads, 2)
+ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
+{
+    extern __shared__ __align__(1024) unsigned char dw_sm[];
+    unsigned char *sm = dw_sm;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + DwSmem::kBar);
+    // loads (k, workspace block: two stages each), products, and the compute warps' arrivals
+    uint64_t *bar_k = bars, *bar_b = bars + 2, *bar_q = bars + 4, *bar_v = bars + 5, *bar_p = bars + 6,
+             *bar_kh = bars + 7, *bar_u = bars + 8, *bar_qh = bars + 9, *bar_y = bars + 10, *bar_dh = bars + 11;
+    uint64_t *arr_h = bars + 12, *arr_q = bars + 13, *arr_r = bars + 14, *arr_u = bars + 15;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const bool issuer = warp == kDwComputeWarps;
+    const int tile = int(blockIdx.x % unsigned(a.col_tiles));
+    const int64_t bh = blockIdx.x / unsigned(a.col_tiles);
+    const int64_t b = bh / a.heads_v;
+    const int h = int(bh % a.heads_v), hk = h / a.ratio;
+    const int n0 = 128 * tile;
+    const uint32_t s_base = smem_u32(sm);
+
+    if (tid == 0) {
+        for (int i = 0; i < 12; ++i)
+            mbar_init(bars + i, 1);
+        for (int i = 12; i < 16; ++i)
+            mbar_init(bars + i, kDwComputeWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, kDwTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
+    // (the swizzled tiles need a 1024-byte aligned base; shared memory starts at one)
+    bool ok = (s_base & 1023u) == 0;
+    if (!ok && tid == 0)
+        atomicOr(status, 1u << kStatusTimeout);
+
+    if (ok && issuer) {
+        // ======================= the issuer warp (one thread works) =======================
+        if (elect_one()) {
+            const int32_t b32 = int32_t(b);
+            const unsigned char *blocks = a.blocks + bh * a.nchunks * kDcBlockBytes;
+            auto load_kb = [&](int c) {
+                const int st = c & 1, t = c * kDcChunk;
+                mbar_arrive_expect_tx(bar_k + st, 16384);
+                tma_load_4d(sm + DwSmem::kK + st * 16384, &maps.k, 0, hk, t, b32, bar_k + st);
+                tma_load_4d(sm + DwSmem::kK + st * 16384 + 8192, &maps.k, 64, hk, t, b32, bar_k + st);
+                mbar_arrive_expect_tx(bar_b + st, kDcHead);
+                bulk_load(sm + DwSmem::kB + st * kDcHead, blocks + int64_t(c) * kDcBlockBytes, kDcHead, bar_b + st);
+            };
+            auto load_p = [&](int c) {
+                mbar_arrive_expect_tx(bar_p, kDcMat);
+                bulk_load(sm + DwSmem::kP, blocks + int64_t(c) * kDcBlockBytes + kDcP, kDcMat, bar_p);
+            };
+            auto load_q = [&](int c) {
+                mbar_arrive_expect_tx(bar_q, 16384);
+                tma_load_4d(sm + DwSmem::kQ, &maps.q, 0, hk, c * kDcChunk, b32, bar_q);
+                tma_load_4d(sm + DwSmem::kQ + 8192, &maps.q, 64, hk, c * kDcChunk, b32, bar_q);
+            };
+            auto load_v = [&](int c) {
+                mbar_arrive_expect_tx(bar_v, 16384);
+                tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, c * kDcChunk, b32, bar_v);
+            };
+            constexpr uint32_t kIdTok = idesc_bf16(128, kDcChunk, 0, 0), kIdHalf = idesc_bf16(128, 32, 0, 0);
+            const uint32_t id_dh = idesc_bf16(128, 16 * a.nks, 0, 1);
+            // phases begun per barrier, for draining after a timeout
+            int nk0 = 1, nk1 = 0, nq = 1, nv = 1, np = 1, nkh = 0, nu = 0, nqh = 0, ny = 0, ndh = 0;
+            load_kb(0);
+            load_q(0);
+            load_v(0);
+            load_p(0);
+            if (a.nchunks > 1) {
+                load_kb(1);
+                nk1 = 1;
+            }
+            for (int c = 0; c < a.nchunks; ++c) {
+                const int st = c & 1;
+                const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
+                const uint32_t kb = s_base + DwSmem::kK + st * 16384, bb = s_base + DwSmem::kB + st * kDcHead;
+                // KH^T once the tile has landed and H(c) is written
+                if (!mbar_wait(bar_k + st, ph2, status) || !mbar_wait(arr_h, ph, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int ks = 0; ks < a.nks; ++ks) {
+                    const uint64_t kd = sw128_desc(kb + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024);
+                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, kd, kIdTok, ks > 0);
+                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks + 8, kd, kIdTok, 1);
+                }
+                umma_commit(bar_kh);
+                nkh = c + 1;
+                // the products of c - 1, the last readers of the other stage and of P, completed
+                // before H(c) was written
+                if (c > 0) {
+                    load_p(c);
+                    np = c + 1;
+                    if (c + 1 < a.nchunks) {
+                        load_kb(c + 1);
+                        ((c + 1) & 1 ? nk1 : nk0) = ((c + 1) >> 1) + 1;
+                    }
+                }
+                // U^T once R is written: the blocks of T on and below the diagonal
+                if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int ks = 0; ks < 2 + 2 * hf; ++ks) {
+                        const uint32_t dst = tmem + kDwD2 + 32 * hf, rhi = tmem + kDwD1 + 16 * ks, rlo = rhi + 8;
+                        const uint32_t to = bb + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0);
+                        const uint64_t thi = sw32_desc(to + kDcThi), tlo = sw32_desc(to + kDcTlo);
+                        umma_bf16_ts(dst, rhi, thi, kIdHalf, ks > 0);
+                        umma_bf16_ts(dst, rlo, thi, kIdHalf, 1);
+                        umma_bf16_ts(dst, rhi, tlo, kIdHalf, 1);
+                    }
+                }
+                umma_commit(bar_u);
+                nu = c + 1;
+                if (c + 1 < a.nchunks) { // R(c), the only reader of v, is written
+                    load_v(c + 1);
+                    nv = c + 2;
+                }
+                // Y^T over R: H^T (sQ)^T, once R has been read
+                if (!mbar_wait(arr_q, ph, status) || !mbar_wait(bar_u, ph, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int ks = 0; ks < a.nks; ++ks) {
+                    const uint32_t qo = s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32;
+                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
+                    umma_bf16_ts(tmem + kDwD1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf,
+                                 ks > 0);
+                }
+                umma_commit(bar_qh);
+                nqh = c + 1;
+                // + U^T P^T, and dH^T over H, once U is written and H has been read
+                if (!mbar_wait(bar_p, ph, status) || !mbar_wait(arr_u, ph, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int ks = 0; ks < 2 + 2 * hf; ++ks)
+                        umma_bf16(tmem + kDwD1 + 32 * hf, sw128_desc(s_base + DwSmem::kU + 32 * ks, 16, 1024),
+                                  sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
+                umma_commit(bar_y);
+                ny = c + 1;
+                if (!mbar_wait(bar_qh, ph, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t kd = sw128_desc(kb + ks * 2048, 8192, 1024); // keys x 16 tokens (MN-major)
+                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks, kd, id_dh, ks > 0);
+                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks + 8, kd, id_dh, 1);
+                }
+                umma_commit(bar_dh);
+                ndh = c + 1;
+                if (c + 1 < a.nchunks) {
+                    load_q(c + 1);
+                    nq = c + 2;
+                }
+            }
+            // let every load and product in flight finish before the tensor memory is freed
+            mbar_wait(bar_k, uint32_t((nk0 - 1) & 1), nullptr);
+            mbar_wait(bar_b, uint32_t((nk0 - 1) & 1), nullptr);
+            if (nk1) {
+                mbar_wait(bar_k + 1, uint32_t((nk1 - 1) & 1), nullptr);
+                mbar_wait(bar_b + 1, uint32_t((nk1 - 1) & 1), nullptr);
+            }
+            mbar_wait(bar_q, uint32_t((nq - 1) & 1), nullptr);
+            mbar_wait(bar_v, uint32_t((nv - 1) & 1), nullptr);
+            mbar_wait(bar_p, uint32_t((np - 1) & 1), nullptr);
+            if (nkh)
+                mbar_wait(bar_kh, uint32_t((nkh - 1) & 1), nullptr);
+            if (nu)
+                mbar_wait(bar_u, uint32_t((nu - 1) & 1), nullptr);
+            if (nqh)
+                mbar_wait(bar_qh, uint32_t((nqh - 1) & 1), nullptr);
+            if (ny)
+                mbar_wait(bar_y, uint32_t((ny - 1) & 1), nullptr);
+            if (ndh)
+                mbar_wait(bar_dh, uint32_t((ndh - 1) & 1), nullptr);
+        }
+    } else if (ok) {
+        // ======================= the compute warps =======================================
+        // warp w: tensor-memory lanes 32 (w % 4) .., half cg = w / 4 of the columns (keys
+        // 64 cg .. of H, tokens 32 cg .. of the chunk)
+        const int q4 = warp & 3, cg = warp >> 2;
+        const int row = 32 * q4 + lane, col = n0 + row; // this thread's value column
+        const bool live = col < a.dv;
+        const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16);
+        float2 H[32]; // keys 64 cg + 2 i, + 1
+        const int64_t sofs = (bh * a.dk + 64 * cg) * a.dv + col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const bool x = live && a.h0 && 64 * cg + 2 * i < a.dk; // (dk is even)
+            H[i] = make_float2(x ? a.h0[sofs + int64_t(2 * i) * a.dv] : 0.0f,
+                               x ? a.h0[sofs + int64_t(2 * i + 1) * a.dv] : 0.0f);
+        }
+        auto store_h = [&](int q) { // keys 16 q .. of this half into their operand columns
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                dw_split2(H[8 * q + e], w[e], w[8 + e]);
+            tmem_st16(lanes + kDwH + 64 * cg + 16 * q, w);
+        };
+        auto arrive = [&](uint64_t *bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            const bool good = __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+            tc_fence_after();
+            return good;
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            store_h(q);
+        tmem_st_wait();
+        arrive(arr_h);
+        for (int c = 0; c < a.nchunks; ++c) {
+            const int st = c & 1;
+            const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
+            const unsigned char *blk = sm + DwSmem::kB + st * kDcHead;
+            const float *sc = reinterpret_cast<const float *>(blk + kDcC);
+            const float *sw = reinterpret_cast<const float *>(blk + kDcW);
+            const float *ss_ = reinterpret_cast<const float *>(blk + kDcS);
+            // ---- while KH^T runs: s o Q in place (bf16) -----------------------------------
+            ok = ok && wait(bar_b + st, ph2) && wait(bar_q, ph);
+            float e_end = 0.0f;
+            if (ok) {
+                e_end = *reinterpret_cast<const float *>(blk + kDcE);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = tid + 32 * kDwComputeWarps * i; // 16-byte chunk: tile, token, position
+                    const float s = ss_[(e >> 3) & 63];
+                    uint4 *p = reinterpret_cast<uint4 *>(sm + DwSmem::kQ + 16 * e);
+                    const uint4 v = *p;
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        o[x] = pack_bf16x2(s * __uint_as_float(in[x] << 16), s * __uint_as_float(in[x] & 0xffff0000u));
+                    *p = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_smem();
+                arrive(arr_q);
+            }
+            // the store of the last chunk's outputs has read its tile: U may go there
+            if (c > 0) {
+                if (tid == 0)
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (!dw_compute_sync_and(ok)) {
+                    ok = false;
+                    break;
+                }
+            }
+            // ---- R^T = V^T - KH^T diag(c) -------------------------------------------------
+            ok = ok && wait(bar_v, ph) && wait(bar_kh, ph);
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int t = 32 * cg + 16 * q;
+                    uint32_t r[16];
+                    tmem_ld16_issue(lanes + kDwD1 + t, r);
+                    const unsigned short *v = reinterpret_cast<const unsigned short *>(sm + DwSmem::kV) + t * 128 + row;
+                    float2 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = make_float2(__uint_as_float(uint32_t(v[256 * e]) << 16),
+                                           __uint_as_float(uint32_t(v[256 * e + 128]) << 16));
+                    tmem_ld_wait();
+                    tmem_ld_fence(r);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 cv = *reinterpret_cast<const float4 *>(sc + t + 2 * e);
+                        dw_split2(__ffma2_rn(make_float2(-cv.x, -cv.y), dw_pair(r, e), x[e]), w[e], w[8 + e]);
+                        dw_split2(__ffma2_rn(make_float2(-cv.z, -cv.w), dw_pair(r, e + 1), x[e + 1]), w[e + 1], w[9 + e]);
+                    }
+                    tmem_st16(lanes + kDwD1 + t, w);
+                }
+                tmem_st_wait();
+                arrive(arr_r);
+            }
+            // ---- U^T: high parts to shared memory, w o U over it --------------------------
+            ok = ok && wait(bar_u, ph);
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int t = 32 * cg + 16 * q;
+                    uint32_t r[16];
+                    tmem_ld16_issue(lanes + kDwD2 + t, r);
+                    tmem_ld_wait();
+                    tmem_ld_fence(r);
+                    uint32_t u[8], w[16];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        u[e] = pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                    *reinterpret_cast<uint4 *>(sm + DwSmem::kU + sw128_off(row, t / 8)) = make_uint4(u[0], u[1], u[2], u[3]);
+                    *reinterpret_cast<uint4 *>(sm + DwSmem::kU + sw128_off(row, t / 8 + 1)) =
+                        make_uint4(u[4], u[5], u[6], u[7]);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 wv = *reinterpret_cast<const float4 *>(sw + t + 2 * e);
+                        dw_split2(__fmul2_rn(make_float2(wv.x, wv.y), dw_pair(r, e)), w[e], w[8 + e]);
+                        dw_split2(__fmul2_rn(make_float2(wv.z, wv.w), dw_pair(r, e + 1)), w[e + 1], w[9 + e]);
+                    }
+                    tmem_st16(lanes + kDwD2 + t, w);
+                }
+                tmem_st_wait();
+                fence_proxy_async_smem();
+                arrive(arr_u);
+            }
+            // ---- while dH^T runs: the outputs ---------------------------------------------
+            ok = ok && wait(bar_y, ph);
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int t = 32 * cg + 16 * q;
+                    uint32_t r[16];
+                    tmem_ld16_issue(lanes + kDwD1 + t, r);
+                    tmem_ld_wait();
+                    tmem_ld_fence(r);
+                    unsigned short *yt = reinterpret_cast<unsigned short *>(sm + DwSmem::kU) + t * 128 + row;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t o = pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                        yt[256 * e] = (unsigned short)(o & 0xffffu);
+                        yt[256 * e + 128] = (unsigned short)(o >> 16);
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            if (!dw_compute_sync_and(ok)) {
+                ok = false;
+                break;
+            }
+            if (tid == 0) {
+                tma_store_4d(&maps.y, sm + DwSmem::kU, n0, h, c * kDcChunk, int32_t(b));
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            // ---- H = E_63 H + dH -------------------------------------------------------------
+            ok = ok && wait(bar_dh, ph);
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (64 * cg + 16 * q < 16 * a.nks) {
+                        uint32_t r[16];
+                        tmem_ld16_issue(lanes + kDwH + 64 * cg + 16 * q, r);
+                        tmem_ld_wait();
+                        tmem_ld_fence(r);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            H[8 * q + e] = __ffma2_rn(make_float2(e_end, e_end), H[8 * q + e], dw_pair(r, e));
+                        store_h(q);
+                    }
+                }
+                tmem_st_wait();
+                arrive(arr_h);
+            }
+        }
+        if (tid == 0) // the tile must not go away under a store
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (ok && live && a.final_state) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (64 * cg + 2 * i < a.dk) {
+                    a.final_state[sofs + int64_t(2 * i) * a.dv] = H[i].x;
+                    a.final_state[sofs + int64_t(2 * i + 1) * a.dv] = H[i].y;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_dealloc(tmem, kDwTmemCols);
+}
+
+} // namespace ss

@@ -10,6 +10,8 @@ less than 40 roundings of 2^-24 to a state that the delta rule does not amplify 
 below 300 * 40 * 6e-8 = 7e-4 if all had one sign and 1e-5 as they fall.  A bfloat16
 output's: half a step of the output, 2^-8 |ref|, and up to three operands rounded to
 bfloat16 whose errors (2^-8 of each term at most) add up over 128 signed terms."""
+import math
+
 import pytest
 import torch
 
@@ -38,12 +40,12 @@ def _scan(inp, **kw):
     return out["outputs"].cpu(), out["final_state"].cpu()
 
 
-def _check(orc, inp, what="", scale=1.0, qk_l2norm=True, **kw):
+def _check(orc, inp, what="", scale=1.0, qk_l2norm=True, grow=1.0, **kw):
     y, fs = _scan(inp, scale=scale, qk_l2norm=qk_l2norm, **kw)
     ref = orc.delta_scan(**inp, scale=scale, qk_l2norm=qk_l2norm)
     assert y.dtype == inp["q"].dtype and fs.dtype == F32
-    assert_close(y, ref["outputs"], TOL[y.dtype], f"{what} outputs")
-    assert_close(fs, ref["final_state"], TOL[F32], f"{what} final_state")
+    assert_close(y, ref["outputs"], grow * TOL[y.dtype], f"{what} outputs")
+    assert_close(fs, ref["final_state"], grow * TOL[F32], f"{what} final_state")
     return y, fs
 
 
@@ -106,7 +108,11 @@ def test_exact_gates(orc, dtype, pattern):
     inp["g"], inp["beta"] = g, beta
     if inp["reset"] is not None:        # the oracle keeps the type, the binding takes both
         inp["reset"] = inp["reset"].to(torch.uint8)
-    _check(orc, inp, pattern)
+    # growing: ten decays of e^0.3 make the state, and with it every term of an output and
+    # its rounding, up to e^3 times what the tolerance is meant for: 128 terms q_i H_ij of
+    # |q| = 1 and columns of length 0.3 sqrt(128) e^3 = 68, each rounded by up to 2^-8, may
+    # differ by 0.27 in all, whatever their sum is
+    _check(orc, inp, pattern, grow=math.exp(3.0) if pattern == "growing" else 1.0)
 
 
 def test_reset_forgets_what_came_before():
