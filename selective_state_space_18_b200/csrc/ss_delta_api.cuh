@@ -87,16 +87,16 @@ bool delta_chunked(const ss::DeltaArgs &a, const void *workspace)
            int64_t(a.heads_v) * a.dv * a.seq < (int64_t(1) << 38); // (byte strides of a tensor map end at 2^40)
 }
 
-// 4-D map (d, head, token, batch) over rows of heads, box (box_d, 1, 64 tokens, 1).
+// 4-D map (d, head, token, batch) over rows of heads, box (box_d, 1, box_t tokens, 1).
 bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, int64_t seq, int64_t batch,
-                  int64_t stride, uint32_t box_d, CUtensorMapSwizzle swizzle)
+                  int64_t stride, uint32_t box_d, uint32_t box_t, CUtensorMapSwizzle swizzle)
 {
     PFN_cuTensorMapEncodeTiled enc = tensor_map_encoder();
     if (!enc)
         return false;
     const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(seq), cuuint64_t(batch)};
     const cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(stride) * 2, cuuint64_t(stride) * 2 * cuuint64_t(seq)};
-    const cuuint32_t box[4] = {box_d, 1, uint32_t(ss::kDcChunk), 1}, estr[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {box_d, 1, box_t, 1}, estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -129,6 +129,8 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     w.nks = (a.dk + 15) / 16;
     w.blocks = p.blocks;
     w.h0 = a.h0;
+    w.g = a.g;
+    w.reset = a.reset;
     w.final_state = a.final_state;
     int64_t units = 0, grid = 0;
     if (!mul_ok(a.batch * a.heads_k, p.nchunks, &units) || units > 0x7fffffffLL ||
@@ -136,11 +138,13 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
         return SS_ERR_SHAPE;
     ss::DeltaWalkMaps maps;
     memset(&maps, 0, sizeof(maps));
-    if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 128,
-                      CU_TENSOR_MAP_SWIZZLE_NONE))
+    constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    constexpr uint32_t kC = ss::kDcChunk;
+    if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride, 64, kC, k128) ||
+        !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride, 64, kC, k128) ||
+        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 64, kC, k128) ||
+        !encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 32, 32,
+                      CU_TENSOR_MAP_SWIZZLE_64B))
         return SS_ERR_CUDA;
     ss::ss_delta_prep_kernel<<<unsigned(units), ss::kDpThreads, ss::DeltaPrepSmem::kBytes, s>>>(p);
     if ((st = launch_status()) != SS_OK)

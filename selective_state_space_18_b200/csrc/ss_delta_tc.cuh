@@ -25,20 +25,26 @@
 // through shared memory, and its right operand straight from the TMA tiles of k and q:
 //   KH^T [128 x 64]  = H^T K^T              R^T = V^T - KH^T diag(c)
 //   U^T  [128 x 64]  = R^T T^T              (only the blocks of T on and below the diagonal)
-//   Y^T  [128 x 64]  = H^T (sQ)^T + U^T P^T
+//   Y^T  [128 x 64]  = (H^T Q^T + U^T P'^T) diag(s),   P'_ij = P_ij / s_i = r_j D_ij/E_i q_i.k_j
 //   dH^T [128 x dk]  = (w o U)^T K          H = E_63 H + dH
+// P' is only in range where the chunk's decays are: with a cut in the chunk, or decays
+// beyond 2^-60 in all, the walk scales the rows of Q by s in shared memory instead and
+// takes P itself (the block says which).
 //
 // Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
 // state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
 // products summed in fp32, so the final state follows fp32 arithmetic to about 5e-6 of
-// its size.  On the way to the outputs, which are rounded to bf16 anyway, H, sQ, P and U
-// enter rounded to bf16 once each (output error 3e-3 of the norm in all, the rounding of
-// the output itself being 1.7e-3).
+// its size.  On the way to the outputs, which are rounded to bf16 anyway, H, P and U enter
+// rounded to bf16 once each (output error 2.7e-3 of the norm in all, the rounding of the
+// output itself being 1.7e-3).
 //
 // Decays.  The cumulative log2 decays are kept as a part of multiples of 1/64, which sums
 // and differences exactly, and a remainder below 1/128 a token, so the decay between two
 // tokens is exact to 1e-7 however much the chunk decays in all.  A token whose decay is
 // zero in fp32 (a reset, -inf, below 2^-160) cuts: cut counts tell which pairs it parts.
+// A cut at a chunk's first token leaves the chunk itself alone: the chunk before it hands
+// on a state of zero (and h0 is not read).  A sequence without h0 begins the same way, so
+// a document that starts a chunk gives the same bits as on its own.
 #pragma once
 
 #include <cuda.h>
@@ -52,7 +58,8 @@ namespace ss {
 
 constexpr int kDcChunk = 64; // tokens per chunk
 
-// A block: T hi, T lo, four arrays of 64 floats (c, w, s and E_63), then P.  A matrix is
+// A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63 and the mode: 0 for
+// P', 1 for P and scaled rows of Q), then P' or P.  A matrix is
 // four slices ks of 32-byte rows in the 32-byte swizzle: columns 16 ks .. 16 ks + 15, rows
 // 0..63 of the first two slices and 32..63 of the last two (the rest is above the diagonal
 // and 0).  Products with it accumulate into two halves of 32 tokens each, always with
@@ -86,6 +93,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Whether the state is discarded before token `tok` (an index over all batch rows).
+__device__ __forceinline__ bool dc_cut(const uint8_t *reset, const float *g, int64_t tok, int heads_v, int h)
+{
+    return (reset && reset[tok]) || (g && __ldg(g + tok * heads_v + h) * kLog2e < -160.0f);
 }
 
 struct DeltaPrepArgs {
@@ -243,8 +256,8 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
                 be = d.beta ? __ldg(d.beta + gi) : 1.0f;
                 const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
                 if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
-                    cut = 1;
-                } else {
+                    cut = tid > 0; // (at the first token: see above)
+                } else if (tid > 0 || chunk > 0 || d.h0) {
                     gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
                     gl = g2 - gh;
                 }
@@ -264,6 +277,8 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
                 sRed[1] = gl;
                 sRed[2] = __int_as_float(cut);
             }
+            if (tid == 0)
+                sRed[3] = t0 + kDcChunk < d.seq && dc_cut(d.reset, d.g, tok0 + kDcChunk, d.heads_v, h) ? 0.0f : 1.0f;
         }
         __syncthreads(); // the tiles, or the previous head's T and P, have been read too
         if (tid < 64) {
@@ -277,15 +292,20 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
             sN[tid] = cut;
             sBeta[tid] = be;
         }
-        __syncthreads();
+        // whether E and 1 / E are in range over the whole chunk
+        const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f)));
         if (tid < 64) {
             const float e = cut ? 0.0f : ex2(gh + gl);
             const float r = sR[tid];
             reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
             reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
+            const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
             reinterpret_cast<float *>(blk + kDcW)[tid] =
-                cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
-            reinterpret_cast<float *>(blk + kDcE)[tid] = sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
+                hand && cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
+            if (tid == 0) {
+                reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
+                reinterpret_cast<float *>(blk + kDcE)[1] = direct ? 1.0f : 0.0f;
+            }
         }
         // ---- A and P ---------------------------------------------------------------------
         {
@@ -298,6 +318,10 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
                 gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
                 bi[x] = sBeta[i] * sR[i];
                 pi[x] = sP[i];
+                if (!direct) {
+                    bi[x] *= ex2(gih[x] + gil[x]);
+                    pi[x] = 1.0f;
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
@@ -307,18 +331,23 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
                     const float2 gjl = *reinterpret_cast<const float2 *>(sGl + j);
                     const int2 nj = *reinterpret_cast<const int2 *>(sN + j);
                     const float2 rj = *reinterpret_cast<const float2 *>(sR + j);
+                    // the decays factor through the chunk's start where E is in range
+                    const float fx = rj.x * ex2(-(gjh.x + gjl.x)), fy = rj.y * ex2(-(gjh.y + gjl.y));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int i = i0 + 8 * x;
-                        const float dx = j <= i && nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
-                        const float dy = j + 1 <= i && nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y))
-                                                                     : 0.0f;
+                        float dx = fx, dy = fy;
+                        if (direct) {
+                            dx = nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
+                            dy = nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y)) : 0.0f;
+                        }
                         if (nt / 2 <= warp)
                             *reinterpret_cast<float2 *>(sA + i * kDpARow + j) =
                                 make_float2(j < i ? bi[x] * dx * kk[nt][2 * x] : 0.0f,
                                             j + 1 < i ? bi[x] * dy * kk[nt][2 * x + 1] : 0.0f);
                         *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) =
-                            pack_bf16x2(pi[x] * dx * qk[nt][2 * x], pi[x] * dy * qk[nt][2 * x + 1]);
+                            pack_bf16x2(j <= i ? pi[x] * dx * qk[nt][2 * x] : 0.0f,
+                                        j + 1 <= i ? pi[x] * dy * qk[nt][2 * x + 1] : 0.0f);
                     }
                 }
             }
@@ -426,18 +455,19 @@ constexpr uint32_t kDwTmemCols = 256;                 // two CTAs per SM
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
 // then R^T over it in the same form (16 columns per 16 tokens), then Y^T.  D2: U^T, then
-// (w o U)^T over it.
-constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192;
+// (w o U)^T over it.  U: U^T rounded, for Y, in the places of remainders of H that KH^T has
+// read (8 columns per 16 tokens, 16 columns apart).
+constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192, kDwU = 72;
 
 struct DwSmem { // from a 1024-byte aligned base
-    static constexpr int kK = 0;                  // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
-    static constexpr int kQ = kK + 2 * 16384;     // q chunk, scaled in place: two tiles
-    static constexpr int kV = kQ + 16384;         // v chunk: [64 tokens x 128 values], not swizzled
-    static constexpr int kU = kV + 16384;         // U^T high parts [128 values x 64 tokens], then Y [64 x 128]
-    static constexpr int kB = kU + 16384;         // workspace blocks up to P: 2 stages
-    static constexpr int kP = kB + 2 * kDcHead;   // P
+    static constexpr int kK = 0;                // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
+    static constexpr int kQ = kK + 2 * 16384;   // q chunk: two tiles
+    static constexpr int kV = kQ + 16384;       // v chunk: two [64 tokens x 64 values] tiles
+    static constexpr int kY = kV + 16384;       // outputs: a [32 tokens x 32 values] tile per compute warp
+    static constexpr int kB = kY + 16384;       // workspace blocks up to P: 2 stages
+    static constexpr int kP = kB + 2 * kDcHead; // P
     static constexpr int kBar = kP + kDcMat;
-    static constexpr int kTmem = kBar + 128;
+    static constexpr int kTmem = kBar + 144;
     static constexpr int kBytes = kBar + 256;
 };
 // two CTAs on an SM: 228 KB, 1 KB of it reserved for each
@@ -449,11 +479,13 @@ struct DeltaWalkArgs {
     int nchunks, col_tiles, nks;  // nks: 16-key slices of the state
     const unsigned char *blocks;
     const float *h0;              // nullable
+    const float *g;               // nullable; g and reset for the first token
+    const uint8_t *reset;         // nullable
     float *final_state;           // nullable
 };
 
 struct DeltaWalkMaps {
-    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), v and y (128, 1, 64, 1)
+    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), y (32, 1, 32, 1)
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
@@ -508,18 +540,45 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void 
                  "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
                  : "memory");
 }
-// Barrier over the compute warps with an AND over every thread's predicate, so that after
-// a failed wait they leave the chunk loop together (a warp that left alone would strand
-// the others at the barrier).
-__device__ __forceinline__ bool dw_compute_sync_and(bool v)
+// The element-wise steps hold tiles of 16 lanes as the warp-wide fragments that
+// tcgen05.ld.16x256b, tcgen05.st.16x128b, ldmatrix and stmatrix share: thread t has rows
+// t / 4 and t / 4 + 8 (x = 0, 1), and of every 8 columns the pair 2 (t % 4), + 1.
+// 32 fp32 columns: r[4 k + 2 x + e] is column 8 k + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16])
 {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                 "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(uint32_t(v)), "n"(32 * kDwComputeWarps)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+    tmem_ld_wait();
+    tmem_ld_fence(r);
+}
+// 16 columns of packed pairs, those of 8 k in columns 4 k .. : r[2 k + x]
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-    return r != 0;
+}
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[4]) // 8 columns
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kDwThreads, 2)
@@ -530,8 +589,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + DwSmem::kBar);
     // loads (k, workspace block: two stages each), products, and the compute warps' arrivals
     uint64_t *bar_k = bars, *bar_b = bars + 2, *bar_q = bars + 4, *bar_v = bars + 5, *bar_p = bars + 6,
-             *bar_kh = bars + 7, *bar_u = bars + 8, *bar_qh = bars + 9, *bar_y = bars + 10, *bar_dh = bars + 11;
-    uint64_t *arr_h = bars + 12, *arr_q = bars + 13, *arr_r = bars + 14, *arr_u = bars + 15;
+             *bar_kh = bars + 7, *bar_u = bars + 8, *bar_qh = bars + 9, *bar_y = bars + 10, *bar_dh = bars + 11 /* [2] */;
+    uint64_t *arr_h = bars + 13, *arr_q = bars + 14, *arr_r = bars + 15, *arr_u = bars + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -544,9 +603,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     const uint32_t s_base = smem_u32(sm);
 
     if (tid == 0) {
-        for (int i = 0; i < 12; ++i)
+        for (int i = 0; i < 13; ++i)
             mbar_init(bars + i, 1);
-        for (int i = 12; i < 16; ++i)
+        for (int i = 13; i < 17; ++i)
             mbar_init(bars + i, kDwComputeWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -588,18 +647,21 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             auto load_v = [&](int c) {
                 mbar_arrive_expect_tx(bar_v, 16384);
                 tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, c * kDcChunk, b32, bar_v);
+                tma_load_4d(sm + DwSmem::kV + 8192, &maps.v, n0 + 64, h, c * kDcChunk, b32, bar_v);
             };
             constexpr uint32_t kIdTok = idesc_bf16(128, kDcChunk, 0, 0), kIdHalf = idesc_bf16(128, 32, 0, 0);
-            const uint32_t id_dh = idesc_bf16(128, 16 * a.nks, 0, 1);
+            // dH in halves of 64 keys
+            const int nk0 = a.nks < 4 ? a.nks : 4;
+            const uint32_t id_dh0 = idesc_bf16(128, 16 * nk0, 0, 1), id_dh1 = idesc_bf16(128, 16 * (a.nks - nk0), 0, 1);
             // phases begun per barrier, for draining after a timeout
-            int nk0 = 1, nk1 = 0, nq = 1, nv = 1, np = 1, nkh = 0, nu = 0, nqh = 0, ny = 0, ndh = 0;
+            int nl0 = 1, nl1 = 0, nq = 1, nv = 1, np = 1, nkh = 0, nu = 0, nqh = 0, ny = 0, ndh0 = 0, ndh1 = 0;
             load_kb(0);
             load_q(0);
             load_v(0);
             load_p(0);
             if (a.nchunks > 1) {
                 load_kb(1);
-                nk1 = 1;
+                nl1 = 1;
             }
             for (int c = 0; c < a.nchunks; ++c) {
                 const int st = c & 1;
@@ -625,7 +687,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     np = c + 1;
                     if (c + 1 < a.nchunks) {
                         load_kb(c + 1);
-                        ((c + 1) & 1 ? nk1 : nk0) = ((c + 1) >> 1) + 1;
+                        ((c + 1) & 1 ? nl1 : nl0) = ((c + 1) >> 1) + 1;
                     }
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
@@ -652,8 +714,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     load_v(c + 1);
                     nv = c + 2;
                 }
-                // Y^T over R: H^T (sQ)^T, once R has been read
-                if (!mbar_wait(arr_q, ph, status) || !mbar_wait(bar_u, ph, status)) {
+                // Y^T over R: H^T Q^T, once R has been read
+                if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status) || !mbar_wait(bar_u, ph, status)) {
                     ok = false;
                     break;
                 }
@@ -666,7 +728,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
                 umma_commit(bar_qh);
                 nqh = c + 1;
-                // + U^T P^T, and dH^T over H, once U is written and H has been read
+                // + U^T P^T, and dH^T over H, once U is written and H has been read: its first
+                // half while U^T P^T completes, whose U lies in the place of the second
                 if (!mbar_wait(bar_p, ph, status) || !mbar_wait(arr_u, ph, status)) {
                     ok = false;
                     break;
@@ -676,8 +739,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int ks = 0; ks < 2 + 2 * hf; ++ks)
-                        umma_bf16(tmem + kDwD1 + 32 * hf, sw128_desc(s_base + DwSmem::kU + 32 * ks, 16, 1024),
-                                  sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
+                        umma_bf16_ts(tmem + kDwD1 + 32 * hf, tmem + kDwU + 16 * ks,
+                                     sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
                 umma_commit(bar_y);
                 ny = c + 1;
                 if (!mbar_wait(bar_qh, ph, status)) {
@@ -688,22 +751,37 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t kd = sw128_desc(kb + ks * 2048, 8192, 1024); // keys x 16 tokens (MN-major)
-                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks, kd, id_dh, ks > 0);
-                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks + 8, kd, id_dh, 1);
+                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks, kd, id_dh0, ks > 0);
+                    umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks + 8, kd, id_dh0, 1);
                 }
                 umma_commit(bar_dh);
-                ndh = c + 1;
+                ndh0 = c + 1;
+                if (a.nks > 4) {
+                    if (!mbar_wait(bar_y, ph, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t kd = sw128_desc(kb + 8192 + ks * 2048, 8192, 1024);
+                        umma_bf16_ts(tmem + kDwH + 64, tmem + kDwD2 + 16 * ks, kd, id_dh1, ks > 0);
+                        umma_bf16_ts(tmem + kDwH + 64, tmem + kDwD2 + 16 * ks + 8, kd, id_dh1, 1);
+                    }
+                }
+                umma_commit(bar_dh + 1);
+                ndh1 = c + 1;
                 if (c + 1 < a.nchunks) {
                     load_q(c + 1);
                     nq = c + 2;
                 }
             }
             // let every load and product in flight finish before the tensor memory is freed
-            mbar_wait(bar_k, uint32_t((nk0 - 1) & 1), nullptr);
-            mbar_wait(bar_b, uint32_t((nk0 - 1) & 1), nullptr);
-            if (nk1) {
-                mbar_wait(bar_k + 1, uint32_t((nk1 - 1) & 1), nullptr);
-                mbar_wait(bar_b + 1, uint32_t((nk1 - 1) & 1), nullptr);
+            mbar_wait(bar_k, uint32_t((nl0 - 1) & 1), nullptr);
+            mbar_wait(bar_b, uint32_t((nl0 - 1) & 1), nullptr);
+            if (nl1) {
+                mbar_wait(bar_k + 1, uint32_t((nl1 - 1) & 1), nullptr);
+                mbar_wait(bar_b + 1, uint32_t((nl1 - 1) & 1), nullptr);
             }
             mbar_wait(bar_q, uint32_t((nq - 1) & 1), nullptr);
             mbar_wait(bar_v, uint32_t((nv - 1) & 1), nullptr);
@@ -716,31 +794,42 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 mbar_wait(bar_qh, uint32_t((nqh - 1) & 1), nullptr);
             if (ny)
                 mbar_wait(bar_y, uint32_t((ny - 1) & 1), nullptr);
-            if (ndh)
-                mbar_wait(bar_dh, uint32_t((ndh - 1) & 1), nullptr);
+            if (ndh0)
+                mbar_wait(bar_dh, uint32_t((ndh0 - 1) & 1), nullptr);
+            if (ndh1)
+                mbar_wait(bar_dh + 1, uint32_t((ndh1 - 1) & 1), nullptr);
         }
     } else if (ok) {
         // ======================= the compute warps =======================================
-        // warp w: tensor-memory lanes 32 (w % 4) .., half cg = w / 4 of the columns (keys
-        // 64 cg .. of H, tokens 32 cg .. of the chunk)
+        // warp w: tensor-memory lanes 32 (w % 4) .. in two tiles m of 16, half cg = w / 4 of
+        // the columns (keys 64 cg .. of H, tokens 32 cg .. of the chunk)
         const int q4 = warp & 3, cg = warp >> 2;
-        const int row = 32 * q4 + lane, col = n0 + row; // this thread's value column
-        const bool live = col < a.dv;
+        const int tr = lane >> 2, tc = 2 * (lane & 3); // this thread's row and column pair of a fragment
+        const int col = n0 + 32 * q4 + tr;             // its first value column; the others 8 apart
         const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16);
-        float2 H[32]; // keys 64 cg + 2 i, + 1
-        const int64_t sofs = (bh * a.dk + 64 * cg) * a.dv + col;
+        // H[m][k][x]: value column col + 16 m + 8 x, keys 64 cg + 8 k + tc, + 1
+        float2 H[2][8][2];
+        const int64_t sofs = (bh * a.dk + 64 * cg + tc) * a.dv + col;
+        const bool enter = a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const bool x = live && a.h0 && 64 * cg + 2 * i < a.dk; // (dk is even)
-            H[i] = make_float2(x ? a.h0[sofs + int64_t(2 * i) * a.dv] : 0.0f,
-                               x ? a.h0[sofs + int64_t(2 * i + 1) * a.dv] : 0.0f);
-        }
-        auto store_h = [&](int q) { // keys 16 q .. of this half into their operand columns
-            uint32_t w[16];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dw_split2(H[8 * q + e], w[e], w[8 + e]);
-            tmem_st16(lanes + kDwH + 64 * cg + 16 * q, w);
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const bool in = enter && 64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < a.dv; // (dk is even)
+                    const int64_t o = sofs + int64_t(8 * k) * a.dv + 16 * m + 8 * x;
+                    H[m][k][x] = make_float2(in ? a.h0[o] : 0.0f, in ? a.h0[o + a.dv] : 0.0f);
+                }
+        // 16 keys (2 k-blocks from kb) of tile m as operand columns
+        auto store_h = [&](int m, int kb) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    dw_split2(H[m][kb + i][x], w[2 * i + x], w[4 + 2 * i + x]);
+            tmem_st_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 8 * kb, w);
         };
         auto arrive = [&](uint64_t *bar) {
             tc_fence_before();
@@ -754,23 +843,34 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             return good;
         };
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            store_h(q);
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int kb = 0; kb < 8; kb += 2)
+                store_h(m, kb);
         tmem_st_wait();
         arrive(arr_h);
+        const uint32_t v_base = s_base + DwSmem::kV + (q4 >> 1) * 8192; // the tile of this warp's values
+        unsigned char *ytile = sm + DwSmem::kY + warp * 2048;
+        const uint32_t y_base = smem_u32(ytile);
         for (int c = 0; c < a.nchunks; ++c) {
             const int st = c & 1;
             const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
             const unsigned char *blk = sm + DwSmem::kB + st * kDcHead;
-            const float *sc = reinterpret_cast<const float *>(blk + kDcC);
-            const float *sw = reinterpret_cast<const float *>(blk + kDcW);
+            const float *sc = reinterpret_cast<const float *>(blk + kDcC) + 32 * cg + tc;
+            const float *sw = reinterpret_cast<const float *>(blk + kDcW) + 32 * cg + tc;
             const float *ss_ = reinterpret_cast<const float *>(blk + kDcS);
-            // ---- while KH^T runs: s o Q in place (bf16) -----------------------------------
-            ok = ok && wait(bar_b + st, ph2) && wait(bar_q, ph);
-            float e_end = 0.0f;
-            if (ok) {
-                e_end = *reinterpret_cast<const float *>(blk + kDcE);
-#pragma unroll
+            if (!wait(bar_b + st, ph2)) {
+                ok = false;
+                break;
+            }
+            const float2 em = *reinterpret_cast<const float2 *>(blk + kDcE); // E_63, mode
+            // ---- s o Q in place (bf16), in chunks whose decays leave the range of P' ---------
+            if (em.y != 0.0f) {
+                if (!wait(bar_q, ph)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     const int e = tid + 32 * kDwComputeWarps * i; // 16-byte chunk: tile, token, position
                     const float s = ss_[(e >> 3) & 63];
@@ -784,132 +884,155 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     *p = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 fence_proxy_async_smem();
-                arrive(arr_q);
             }
-            // the store of the last chunk's outputs has read its tile: U may go there
-            if (c > 0) {
-                if (tid == 0)
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                if (!dw_compute_sync_and(ok)) {
-                    ok = false;
-                    break;
-                }
-            }
+            arrive(arr_q);
             // ---- R^T = V^T - KH^T diag(c) -------------------------------------------------
-            ok = ok && wait(bar_v, ph) && wait(bar_kh, ph);
-            if (ok) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = 32 * cg + 16 * q;
-                    uint32_t r[16];
-                    tmem_ld16_issue(lanes + kDwD1 + t, r);
-                    const unsigned short *v = reinterpret_cast<const unsigned short *>(sm + DwSmem::kV) + t * 128 + row;
-                    float2 x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = make_float2(__uint_as_float(uint32_t(v[256 * e]) << 16),
-                                           __uint_as_float(uint32_t(v[256 * e + 128]) << 16));
-                    tmem_ld_wait();
-                    tmem_ld_fence(r);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float4 cv = *reinterpret_cast<const float4 *>(sc + t + 2 * e);
-                        dw_split2(__ffma2_rn(make_float2(-cv.x, -cv.y), dw_pair(r, e), x[e]), w[e], w[8 + e]);
-                        dw_split2(__ffma2_rn(make_float2(-cv.z, -cv.w), dw_pair(r, e + 1), x[e + 1]), w[e + 1], w[9 + e]);
-                    }
-                    tmem_st16(lanes + kDwD1 + t, w);
-                }
-                tmem_st_wait();
-                arrive(arr_r);
-            }
-            // ---- U^T: high parts to shared memory, w o U over it --------------------------
-            ok = ok && wait(bar_u, ph);
-            if (ok) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = 32 * cg + 16 * q;
-                    uint32_t r[16];
-                    tmem_ld16_issue(lanes + kDwD2 + t, r);
-                    tmem_ld_wait();
-                    tmem_ld_fence(r);
-                    uint32_t u[8], w[16];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        u[e] = pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                    *reinterpret_cast<uint4 *>(sm + DwSmem::kU + sw128_off(row, t / 8)) = make_uint4(u[0], u[1], u[2], u[3]);
-                    *reinterpret_cast<uint4 *>(sm + DwSmem::kU + sw128_off(row, t / 8 + 1)) =
-                        make_uint4(u[4], u[5], u[6], u[7]);
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float4 wv = *reinterpret_cast<const float4 *>(sw + t + 2 * e);
-                        dw_split2(__fmul2_rn(make_float2(wv.x, wv.y), dw_pair(r, e)), w[e], w[8 + e]);
-                        dw_split2(__fmul2_rn(make_float2(wv.z, wv.w), dw_pair(r, e + 1)), w[e + 1], w[9 + e]);
-                    }
-                    tmem_st16(lanes + kDwD2 + t, w);
-                }
-                tmem_st_wait();
-                fence_proxy_async_smem();
-                arrive(arr_u);
-            }
-            // ---- while dH^T runs: the outputs ---------------------------------------------
-            ok = ok && wait(bar_y, ph);
-            if (ok) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = 32 * cg + 16 * q;
-                    uint32_t r[16];
-                    tmem_ld16_issue(lanes + kDwD1 + t, r);
-                    tmem_ld_wait();
-                    tmem_ld_fence(r);
-                    unsigned short *yt = reinterpret_cast<unsigned short *>(sm + DwSmem::kU) + t * 128 + row;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t o = pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                        yt[256 * e] = (unsigned short)(o & 0xffffu);
-                        yt[256 * e + 128] = (unsigned short)(o >> 16);
-                    }
-                }
-                fence_proxy_async_smem();
-            }
-            if (!dw_compute_sync_and(ok)) {
+            if (!wait(bar_v, ph) || !wait(bar_kh, ph)) {
                 ok = false;
                 break;
             }
-            if (tid == 0) {
-                tma_store_4d(&maps.y, sm + DwSmem::kU, n0, h, c * kDcChunk, int32_t(b));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg;
+                uint32_t r[16], v[2][4];
+                // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (lane >> 4) + (lane & 7),
+                                                               4 * (q4 & 1) + 2 * m + ((lane >> 3) & 1)));
+                tmem_ld_frag(at, r);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = 2 * j + i;
+                        const float2 cv = *reinterpret_cast<const float2 *>(sc + 8 * k);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t vv = v[j][2 * i + x];
+                            dw_split2(__ffma2_rn(make_float2(-cv.x, -cv.y), dw_pair(r, 2 * k + x),
+                                                 make_float2(__uint_as_float(vv << 16), __uint_as_float(vv & 0xffff0000u))),
+                                      w[2 * i + x], w[4 + 2 * i + x]);
+                        }
+                    }
+                    tmem_st_frag(at + 16 * j, w);
+                }
+            }
+            tmem_st_wait();
+            // (before the arrival that the products of this chunk wait for: the store of the
+            // last outputs has read this warp's tile)
+            if (lane == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            arrive(arr_r);
+            // ---- U^T rounded, and w o U over it -----------------------------------------------
+            if (!wait(bar_u, ph)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + 32 * cg;
+                uint32_t r[16];
+                tmem_ld_frag(at, r);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t w[8], u[4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = 2 * j + i;
+                        const float2 wv = *reinterpret_cast<const float2 *>(sw + 8 * k);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 uu = dw_pair(r, 2 * k + x);
+                            u[2 * i + x] = pack_bf16x2(uu.x, uu.y);
+                            dw_split2(__fmul2_rn(wv, uu), w[2 * i + x], w[4 + 2 * i + x]);
+                        }
+                    }
+                    tmem_st_frag(ml + kDwU + 16 * (2 * cg + j), u);
+                    tmem_st_frag(at + 16 * j, w);
+                }
+            }
+            tmem_st_wait();
+            arrive(arr_u);
+            // ---- while dH^T runs: the outputs ---------------------------------------------
+            if (!wait(bar_y, ph)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t r[16];
+                tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg, r);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = 2 * j + i;
+                        float2 sv = make_float2(1.0f, 1.0f);
+                        if (em.y == 0.0f)
+                            sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * k + x));
+                            o[2 * i + x] = pack_bf16x2(y.x, y.y);
+                        }
+                    }
+                    // rows of 64 bytes (32 values) in the 64-byte swizzle: token 8 (2 j + matrix / 2)
+                    // + lane % 8, values 16 m + 8 (matrix % 2) ..
+                    const int t = 16 * j + 8 * (lane >> 4) + (lane & 7), ch = 2 * m + ((lane >> 3) & 1);
+                    stmatrix_x4_trans(y_base + 64 * t + 16 * (ch ^ ((t >> 1) & 3)), o);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (n0 + 32 * q4 < a.dv && int64_t(c) * kDcChunk + 32 * cg < a.seq)
+                    tma_store_4d(&maps.y, ytile, n0 + 32 * q4, h, c * kDcChunk + 32 * cg, int32_t(b));
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             // ---- H = E_63 H + dH -------------------------------------------------------------
-            ok = ok && wait(bar_dh, ph);
-            if (ok) {
+            if (!wait(bar_dh + cg, ph)) {
+                ok = false;
+                break;
+            }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (64 * cg + 16 * q < 16 * a.nks) {
+            for (int hf = 0; hf < 2; ++hf) {
+                if (4 * cg + 2 * hf < a.nks) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
                         uint32_t r[16];
-                        tmem_ld16_issue(lanes + kDwH + 64 * cg + 16 * q, r);
-                        tmem_ld_wait();
-                        tmem_ld_fence(r);
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 32 * hf, r);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            H[8 * q + e] = __ffma2_rn(make_float2(e_end, e_end), H[8 * q + e], dw_pair(r, e));
-                        store_h(q);
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                H[m][4 * hf + k][x] =
+                                    __ffma2_rn(make_float2(em.x, em.x), H[m][4 * hf + k][x], dw_pair(r, 2 * k + x));
+                        store_h(m, 4 * hf);
+                        store_h(m, 4 * hf + 2);
                     }
                 }
-                tmem_st_wait();
-                arrive(arr_h);
             }
+            tmem_st_wait();
+            arrive(arr_h);
         }
-        if (tid == 0) // the tile must not go away under a store
+        if (lane == 0) // the tile must not go away under a store
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        if (ok && live && a.final_state) {
+        if (ok && a.final_state) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (64 * cg + 2 * i < a.dk) {
-                    a.final_state[sofs + int64_t(2 * i) * a.dv] = H[i].x;
-                    a.final_state[sofs + int64_t(2 * i + 1) * a.dv] = H[i].y;
-                }
-            }
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < a.dv) {
+                            const int64_t o = sofs + int64_t(8 * k) * a.dv + 16 * m + 8 * x;
+                            a.final_state[o] = H[m][k][x].x;
+                            a.final_state[o + a.dv] = H[m][k][x].y;
+                        }
+                    }
         }
     }
     tc_fence_before();
