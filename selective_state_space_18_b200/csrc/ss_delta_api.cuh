@@ -102,16 +102,30 @@ bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int MT>
+int launch_delta_walk(const ss::DeltaWalkArgs &w, ss::DeltaWalkMaps &maps, const ss::DeltaArgs &a, unsigned grid,
+                      uint32_t *status, cudaStream_t s)
+{
+    static std::atomic<uint64_t> smem_done{0};
+    const int st = ensure_smem(ss::ss_delta_walk_kernel<MT>, size_t(ss::DwSmem::kBytes), smem_done);
+    if (st != SS_OK)
+        return st;
+    if (!encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 16 * MT, 32,
+                      MT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B))
+        return SS_ERR_CUDA;
+    ss::ss_delta_walk_kernel<MT><<<grid, ss::DwShape<MT>::kThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
+    return launch_status();
+}
+
 int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s)
 {
-    static std::atomic<uint64_t> prep_done{0}, walk_done{0};
-    int st = ensure_smem(ss::ss_delta_prep_kernel, size_t(ss::DeltaPrepSmem::kBytes), prep_done);
-    if (st == SS_OK)
-        st = ensure_smem(ss::ss_delta_walk_kernel, size_t(ss::DwSmem::kBytes), walk_done);
+    static std::atomic<uint64_t> smem_done{0};
+    int st = ensure_smem(ss::ss_delta_prep_kernel, size_t(ss::DeltaPrepSmem::kBytes), smem_done);
     if (st != SS_OK)
         return st;
     uint32_t *status = nullptr;
-    if (status_word_address(&status) != SS_OK)
+    int sms = 0;
+    if (status_word_address(&status) != SS_OK || device_sm_count(&sms) != SS_OK)
         return SS_ERR_CUDA;
     ss::DeltaPrepArgs p{};
     p.d = a;
@@ -142,15 +156,14 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     constexpr uint32_t kC = ss::kDcChunk;
     if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride, 64, kC, k128) ||
         !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride, 64, kC, k128) ||
-        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 64, kC, k128) ||
-        !encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 32, 32,
-                      CU_TENSOR_MAP_SWIZZLE_64B))
+        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 64, kC, k128))
         return SS_ERR_CUDA;
     ss::ss_delta_prep_kernel<<<unsigned(units), ss::kDpThreads, ss::DeltaPrepSmem::kBytes, s>>>(p);
     if ((st = launch_status()) != SS_OK)
         return st;
-    ss::ss_delta_walk_kernel<<<unsigned(grid), ss::kDwThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
-    return launch_status();
+    // up to one walk per SM: sixteen compute warps each; more: two CTAs of eight per SM
+    return grid <= sms ? launch_delta_walk<1>(w, maps, a, unsigned(grid), status, s)
+                       : launch_delta_walk<2>(w, maps, a, unsigned(grid), status, s);
 }
 
 template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cudaStream_t s)

@@ -449,9 +449,13 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
 
 // ---- the walk ------------------------------------------------------------------------
 
-constexpr int kDwComputeWarps = 8;
-constexpr int kDwThreads = 32 * kDwComputeWarps + 32; // + the issuer warp
-constexpr uint32_t kDwTmemCols = 256;                 // two CTAs per SM
+// MT: tiles of 16 lanes per compute warp, 2 (eight compute warps, two CTAs per SM) or 1
+// (sixteen compute warps, one CTA per SM)
+template <int MT> struct DwShape {
+    static constexpr int kWarps = 16 / MT;           // compute warps
+    static constexpr int kThreads = 32 * kWarps + 32; // + the issuer warp
+};
+constexpr uint32_t kDwTmemCols = 256; // (two CTAs per SM)
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
 // then R^T over it in the same form (16 columns per 16 tokens), then Y^T.  D2: U^T, then
@@ -463,7 +467,7 @@ struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kK = 0;                // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
     static constexpr int kQ = kK + 2 * 16384;   // q chunk: two tiles
     static constexpr int kV = kQ + 16384;       // v chunk: two [64 tokens x 64 values] tiles
-    static constexpr int kY = kV + 16384;       // outputs: a [32 tokens x 32 values] tile per compute warp
+    static constexpr int kY = kV + 16384;       // outputs: tiles of [32 tokens x 32 or 16 values], one per compute warp
     static constexpr int kB = kY + 16384;       // workspace blocks up to P: 2 stages
     static constexpr int kP = kB + 2 * kDcHead; // P
     static constexpr int kBar = kP + kDcMat;
@@ -485,7 +489,7 @@ struct DeltaWalkArgs {
 };
 
 struct DeltaWalkMaps {
-    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), y (32, 1, 32, 1)
+    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), y (16 MT, 1, 32, 1)
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
@@ -581,9 +585,11 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t
                  : "memory");
 }
 
-__global__ void __launch_bounds__(kDwThreads, 2)
+template <int MT>
+__global__ void __launch_bounds__(DwShape<MT>::kThreads, MT)
 ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
 {
+    constexpr int kWarps = DwShape<MT>::kWarps;
     extern __shared__ __align__(1024) unsigned char dw_sm[];
     unsigned char *sm = dw_sm;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + DwSmem::kBar);
@@ -594,7 +600,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const bool issuer = warp == kDwComputeWarps;
+    const bool issuer = warp == kWarps;
     const int tile = int(blockIdx.x % unsigned(a.col_tiles));
     const int64_t bh = blockIdx.x / unsigned(a.col_tiles);
     const int64_t b = bh / a.heads_v;
@@ -606,7 +612,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         for (int i = 0; i < 13; ++i)
             mbar_init(bars + i, 1);
         for (int i = 13; i < 17; ++i)
-            mbar_init(bars + i, kDwComputeWarps);
+            mbar_init(bars + i, kWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -627,8 +633,20 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         if (elect_one()) {
             const int32_t b32 = int32_t(b);
             const unsigned char *blocks = a.blocks + bh * a.nchunks * kDcBlockBytes;
+            // barriers with a phase begun by a load or a product, and its parity
+            uint32_t begun = 0, latest = ~0u;
+            auto begin = [&](const uint64_t *bar) {
+                begun |= 1u << int(bar - bars);
+                latest ^= 1u << int(bar - bars);
+            };
+            auto commit = [&](uint64_t *bar) {
+                umma_commit(bar);
+                begin(bar);
+            };
             auto load_kb = [&](int c) {
                 const int st = c & 1, t = c * kDcChunk;
+                begin(bar_k + st);
+                begin(bar_b + st);
                 mbar_arrive_expect_tx(bar_k + st, 16384);
                 tma_load_4d(sm + DwSmem::kK + st * 16384, &maps.k, 0, hk, t, b32, bar_k + st);
                 tma_load_4d(sm + DwSmem::kK + st * 16384 + 8192, &maps.k, 64, hk, t, b32, bar_k + st);
@@ -636,15 +654,18 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 bulk_load(sm + DwSmem::kB + st * kDcHead, blocks + int64_t(c) * kDcBlockBytes, kDcHead, bar_b + st);
             };
             auto load_p = [&](int c) {
+                begin(bar_p);
                 mbar_arrive_expect_tx(bar_p, kDcMat);
                 bulk_load(sm + DwSmem::kP, blocks + int64_t(c) * kDcBlockBytes + kDcP, kDcMat, bar_p);
             };
             auto load_q = [&](int c) {
+                begin(bar_q);
                 mbar_arrive_expect_tx(bar_q, 16384);
                 tma_load_4d(sm + DwSmem::kQ, &maps.q, 0, hk, c * kDcChunk, b32, bar_q);
                 tma_load_4d(sm + DwSmem::kQ + 8192, &maps.q, 64, hk, c * kDcChunk, b32, bar_q);
             };
             auto load_v = [&](int c) {
+                begin(bar_v);
                 mbar_arrive_expect_tx(bar_v, 16384);
                 tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, c * kDcChunk, b32, bar_v);
                 tma_load_4d(sm + DwSmem::kV + 8192, &maps.v, n0 + 64, h, c * kDcChunk, b32, bar_v);
@@ -653,16 +674,12 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             // dH in halves of 64 keys
             const int nk0 = a.nks < 4 ? a.nks : 4;
             const uint32_t id_dh0 = idesc_bf16(128, 16 * nk0, 0, 1), id_dh1 = idesc_bf16(128, 16 * (a.nks - nk0), 0, 1);
-            // phases begun per barrier, for draining after a timeout
-            int nl0 = 1, nl1 = 0, nq = 1, nv = 1, np = 1, nkh = 0, nu = 0, nqh = 0, ny = 0, ndh0 = 0, ndh1 = 0;
             load_kb(0);
             load_q(0);
             load_v(0);
             load_p(0);
-            if (a.nchunks > 1) {
+            if (a.nchunks > 1)
                 load_kb(1);
-                nl1 = 1;
-            }
             for (int c = 0; c < a.nchunks; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
@@ -678,17 +695,13 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, kd, kIdTok, ks > 0);
                     umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks + 8, kd, kIdTok, 1);
                 }
-                umma_commit(bar_kh);
-                nkh = c + 1;
+                commit(bar_kh);
                 // the products of c - 1, the last readers of the other stage and of P, completed
                 // before H(c) was written
                 if (c > 0) {
                     load_p(c);
-                    np = c + 1;
-                    if (c + 1 < a.nchunks) {
+                    if (c + 1 < a.nchunks)
                         load_kb(c + 1);
-                        ((c + 1) & 1 ? nl1 : nl0) = ((c + 1) >> 1) + 1;
-                    }
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
                 if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
@@ -708,12 +721,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                         umma_bf16_ts(dst, rhi, tlo, kIdHalf, 1);
                     }
                 }
-                umma_commit(bar_u);
-                nu = c + 1;
-                if (c + 1 < a.nchunks) { // R(c), the only reader of v, is written
+                commit(bar_u);
+                if (c + 1 < a.nchunks) // R(c), the only reader of v, is written
                     load_v(c + 1);
-                    nv = c + 2;
-                }
                 // Y^T over R: H^T Q^T, once R has been read
                 if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status) || !mbar_wait(bar_u, ph, status)) {
                     ok = false;
@@ -726,8 +736,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     umma_bf16_ts(tmem + kDwD1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf,
                                  ks > 0);
                 }
-                umma_commit(bar_qh);
-                nqh = c + 1;
+                commit(bar_qh);
                 // + U^T P^T, and dH^T over H, once U is written and H has been read: its first
                 // half while U^T P^T completes, whose U lies in the place of the second
                 if (!mbar_wait(bar_p, ph, status) || !mbar_wait(arr_u, ph, status)) {
@@ -741,8 +750,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     for (int ks = 0; ks < 2 + 2 * hf; ++ks)
                         umma_bf16_ts(tmem + kDwD1 + 32 * hf, tmem + kDwU + 16 * ks,
                                      sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
-                umma_commit(bar_y);
-                ny = c + 1;
+                commit(bar_y);
                 if (!mbar_wait(bar_qh, ph, status)) {
                     ok = false;
                     break;
@@ -754,8 +762,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks, kd, id_dh0, ks > 0);
                     umma_bf16_ts(tmem + kDwH, tmem + kDwD2 + 16 * ks + 8, kd, id_dh0, 1);
                 }
-                umma_commit(bar_dh);
-                ndh0 = c + 1;
+                commit(bar_dh);
                 if (a.nks > 4) {
                     if (!mbar_wait(bar_y, ph, status)) {
                         ok = false;
@@ -769,50 +776,32 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                         umma_bf16_ts(tmem + kDwH + 64, tmem + kDwD2 + 16 * ks + 8, kd, id_dh1, 1);
                     }
                 }
-                umma_commit(bar_dh + 1);
-                ndh1 = c + 1;
-                if (c + 1 < a.nchunks) {
+                commit(bar_dh + 1);
+                if (c + 1 < a.nchunks)
                     load_q(c + 1);
-                    nq = c + 2;
-                }
             }
-            // let every load and product in flight finish before the tensor memory is freed
-            mbar_wait(bar_k, uint32_t((nl0 - 1) & 1), nullptr);
-            mbar_wait(bar_b, uint32_t((nl0 - 1) & 1), nullptr);
-            if (nl1) {
-                mbar_wait(bar_k + 1, uint32_t((nl1 - 1) & 1), nullptr);
-                mbar_wait(bar_b + 1, uint32_t((nl1 - 1) & 1), nullptr);
-            }
-            mbar_wait(bar_q, uint32_t((nq - 1) & 1), nullptr);
-            mbar_wait(bar_v, uint32_t((nv - 1) & 1), nullptr);
-            mbar_wait(bar_p, uint32_t((np - 1) & 1), nullptr);
-            if (nkh)
-                mbar_wait(bar_kh, uint32_t((nkh - 1) & 1), nullptr);
-            if (nu)
-                mbar_wait(bar_u, uint32_t((nu - 1) & 1), nullptr);
-            if (nqh)
-                mbar_wait(bar_qh, uint32_t((nqh - 1) & 1), nullptr);
-            if (ny)
-                mbar_wait(bar_y, uint32_t((ny - 1) & 1), nullptr);
-            if (ndh0)
-                mbar_wait(bar_dh, uint32_t((ndh0 - 1) & 1), nullptr);
-            if (ndh1)
-                mbar_wait(bar_dh + 1, uint32_t((ndh1 - 1) & 1), nullptr);
+            // let every load and product in flight finish before the tensor memory is freed:
+            // the latest phase of each barrier
+            for (int i = 0; i < 13; ++i)
+                if ((begun >> i) & 1u)
+                    mbar_wait(bars + i, (latest >> i) & 1u, nullptr);
         }
     } else if (ok) {
         // ======================= the compute warps =======================================
-        // warp w: tensor-memory lanes 32 (w % 4) .. in two tiles m of 16, half cg = w / 4 of
-        // the columns (keys 64 cg .. of H, tokens 32 cg .. of the chunk)
-        const int q4 = warp & 3, cg = warp >> 2;
+        // warp w: MT tiles m of 16 tensor-memory lanes from row0 (a warp reaches the lanes
+        // 32 (w % 4) .. + 31), half cg of the columns (keys 64 cg .. of H, tokens 32 cg .. of
+        // the chunk)
+        const int q4 = warp & 3, cg = (warp >> 2) & 1;
+        const int row0 = 32 * q4 + (MT == 1 ? 16 * (warp >> 3) : 0);
         const int tr = lane >> 2, tc = 2 * (lane & 3); // this thread's row and column pair of a fragment
-        const int col = n0 + 32 * q4 + tr;             // its first value column; the others 8 apart
-        const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16);
+        const int col = n0 + row0 + tr;             // its first value column; the others 8 apart
+        const uint32_t lanes = tmem + (uint32_t(row0) << 16);
         // H[m][k][x]: value column col + 16 m + 8 x, keys 64 cg + 8 k + tc, + 1
-        float2 H[2][8][2];
+        float2 H[MT][8][2];
         const int64_t sofs = (bh * a.dk + 64 * cg + tc) * a.dv + col;
         const bool enter = a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
 #pragma unroll
@@ -843,14 +832,14 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             return good;
         };
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int kb = 0; kb < 8; kb += 2)
                 store_h(m, kb);
         tmem_st_wait();
         arrive(arr_h);
         const uint32_t v_base = s_base + DwSmem::kV + (q4 >> 1) * 8192; // the tile of this warp's values
-        unsigned char *ytile = sm + DwSmem::kY + warp * 2048;
+        unsigned char *ytile = sm + DwSmem::kY + warp * (1024 * MT);
         const uint32_t y_base = smem_u32(ytile);
         for (int c = 0; c < a.nchunks; ++c) {
             const int st = c & 1;
@@ -859,6 +848,10 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             const float *sc = reinterpret_cast<const float *>(blk + kDcC) + 32 * cg + tc;
             const float *sw = reinterpret_cast<const float *>(blk + kDcW) + 32 * cg + tc;
             const float *ss_ = reinterpret_cast<const float *>(blk + kDcS);
+            // the shared-memory addresses of a step are computed when it runs: kept over the
+            // loop they would cost the registers that H needs
+            int ln = lane;
+            asm volatile("" : "+r"(ln));
             if (!wait(bar_b + st, ph2)) {
                 ok = false;
                 break;
@@ -871,8 +864,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     break;
                 }
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int e = tid + 32 * kDwComputeWarps * i; // 16-byte chunk: tile, token, position
+                for (int i = 0; i < 1024 / (32 * kWarps); ++i) {
+                    const int e = tid + 32 * kWarps * i; // 16-byte chunk: tile, token, position
                     const float s = ss_[(e >> 3) & 63];
                     uint4 *p = reinterpret_cast<uint4 *>(sm + DwSmem::kQ + 16 * e);
                     const uint4 v = *p;
@@ -892,14 +885,14 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < MT; ++m) {
                 const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg;
                 uint32_t r[16], v[2][4];
                 // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (lane >> 4) + (lane & 7),
-                                                               4 * (q4 & 1) + 2 * m + ((lane >> 3) & 1)));
+                    ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
+                                                               ((row0 & 63) >> 3) + 2 * m + ((ln >> 3) & 1)));
                 tmem_ld_frag(at, r);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -931,7 +924,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < MT; ++m) {
                 const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + 32 * cg;
                 uint32_t r[16];
                 tmem_ld_frag(at, r);
@@ -961,7 +954,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < MT; ++m) {
                 uint32_t r[16];
                 tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg, r);
 #pragma unroll
@@ -979,17 +972,17 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                             o[2 * i + x] = pack_bf16x2(y.x, y.y);
                         }
                     }
-                    // rows of 64 bytes (32 values) in the 64-byte swizzle: token 8 (2 j + matrix / 2)
-                    // + lane % 8, values 16 m + 8 (matrix % 2) ..
-                    const int t = 16 * j + 8 * (lane >> 4) + (lane & 7), ch = 2 * m + ((lane >> 3) & 1);
-                    stmatrix_x4_trans(y_base + 64 * t + 16 * (ch ^ ((t >> 1) & 3)), o);
+                    // rows of 32 MT bytes (16 MT values) in the swizzle of that span: token 8 (2 j +
+                    // matrix / 2) + lane % 8, values 16 m + 8 (matrix % 2) ..
+                    const int t = 16 * j + 8 * (ln >> 4) + (ln & 7), ch = 2 * m + ((ln >> 3) & 1);
+                    stmatrix_x4_trans(y_base + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1)), o);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (n0 + 32 * q4 < a.dv && int64_t(c) * kDcChunk + 32 * cg < a.seq)
-                    tma_store_4d(&maps.y, ytile, n0 + 32 * q4, h, c * kDcChunk + 32 * cg, int32_t(b));
+                if (n0 + row0 < a.dv && int64_t(c) * kDcChunk + 32 * cg < a.seq)
+                    tma_store_4d(&maps.y, ytile, n0 + row0, h, c * kDcChunk + 32 * cg, int32_t(b));
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             // ---- H = E_63 H + dH -------------------------------------------------------------
@@ -1001,7 +994,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             for (int hf = 0; hf < 2; ++hf) {
                 if (4 * cg + 2 * hf < a.nks) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
+                    for (int m = 0; m < MT; ++m) {
                         uint32_t r[16];
                         tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 32 * hf, r);
 #pragma unroll
@@ -1022,7 +1015,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         if (ok && a.final_state) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
 #pragma unroll
