@@ -87,32 +87,30 @@ bool delta_chunked(const ss::DeltaArgs &a, const void *workspace)
            int64_t(a.heads_v) * a.dv * a.seq < (int64_t(1) << 38); // (byte strides of a tensor map end at 2^40)
 }
 
-// 4-D map (d, head, token, batch) over rows of heads, box (box_d, 1, box_t tokens, 1).
+// 4-D map (d, head, token, batch) over rows of heads, box (64, 1, 64 tokens, 1),
+// 128-byte swizzle.
 bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, int64_t seq, int64_t batch,
-                  int64_t stride, uint32_t box_d, uint32_t box_t, CUtensorMapSwizzle swizzle)
+                  int64_t stride)
 {
     PFN_cuTensorMapEncodeTiled enc = tensor_map_encoder();
     if (!enc)
         return false;
     const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(seq), cuuint64_t(batch)};
     const cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(stride) * 2, cuuint64_t(stride) * 2 * cuuint64_t(seq)};
-    const cuuint32_t box[4] = {box_d, 1, box_t, 1}, estr[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 1, uint32_t(ss::kDcChunk), 1}, estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MT>
-int launch_delta_walk(const ss::DeltaWalkArgs &w, ss::DeltaWalkMaps &maps, const ss::DeltaArgs &a, unsigned grid,
-                      uint32_t *status, cudaStream_t s)
+int launch_delta_walk(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps, unsigned grid, uint32_t *status,
+                      cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
     const int st = ensure_smem(ss::ss_delta_walk_kernel<MT>, size_t(ss::DwSmem::kBytes), smem_done);
     if (st != SS_OK)
         return st;
-    if (!encode_heads(&maps.y, a.y, a.dv, a.heads_v, a.seq, a.batch, int64_t(a.heads_v) * a.dv, 16 * MT, 32,
-                      MT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B))
-        return SS_ERR_CUDA;
     ss::ss_delta_walk_kernel<MT><<<grid, ss::DwShape<MT>::kThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
     return launch_status();
 }
@@ -133,7 +131,7 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     p.blocks = static_cast<unsigned char *>(workspace);
     ss::DeltaWalkArgs w{};
     w.batch = a.batch;
-    w.seq = a.seq;
+    w.seq = int(a.seq);
     w.heads_v = a.heads_v;
     w.ratio = a.ratio;
     w.dk = a.dk;
@@ -145,25 +143,24 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     w.h0 = a.h0;
     w.g = a.g;
     w.reset = a.reset;
+    w.y = static_cast<__nv_bfloat16 *>(a.y);
     w.final_state = a.final_state;
     int64_t units = 0, grid = 0;
-    if (!mul_ok(a.batch * a.heads_k, p.nchunks, &units) || units > 0x7fffffffLL ||
+    if (!mul_ok(a.batch * a.heads_v, p.nchunks, &units) || units > 0x7fffffffLL ||
         !mul_ok(a.batch * a.heads_v, w.col_tiles, &grid) || grid > 0x7fffffffLL)
         return SS_ERR_SHAPE;
     ss::DeltaWalkMaps maps;
     memset(&maps, 0, sizeof(maps));
-    constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B;
-    constexpr uint32_t kC = ss::kDcChunk;
-    if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride, 64, kC, k128) ||
-        !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride, 64, kC, k128) ||
-        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride, 64, kC, k128))
+    if (!encode_heads(&maps.q, a.q, a.dk, a.heads_k, a.seq, a.batch, a.q_stride) ||
+        !encode_heads(&maps.k, a.k, a.dk, a.heads_k, a.seq, a.batch, a.k_stride) ||
+        !encode_heads(&maps.v, a.v, a.dv, a.heads_v, a.seq, a.batch, a.v_stride))
         return SS_ERR_CUDA;
     ss::ss_delta_prep_kernel<<<unsigned(units), ss::kDpThreads, ss::DeltaPrepSmem::kBytes, s>>>(p);
     if ((st = launch_status()) != SS_OK)
         return st;
     // up to one walk per SM: sixteen compute warps each; more: two CTAs of eight per SM
-    return grid <= sms ? launch_delta_walk<1>(w, maps, a, unsigned(grid), status, s)
-                       : launch_delta_walk<2>(w, maps, a, unsigned(grid), status, s);
+    return grid <= sms ? launch_delta_walk<1>(w, maps, unsigned(grid), status, s)
+                       : launch_delta_walk<2>(w, maps, unsigned(grid), status, s);
 }
 
 template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cudaStream_t s)

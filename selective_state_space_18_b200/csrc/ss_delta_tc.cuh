@@ -14,7 +14,7 @@
 // The norms of q and k are factors of rows and columns, so q and k enter every product as
 // they are stored.
 //
-// The preparation (ss_delta_prep_kernel, one CTA per chunk and key head) needs no state:
+// The preparation (ss_delta_prep_kernel, one CTA per chunk and value head) needs no state:
 // K K^T and Q K^T, the decays, T = (I + A)^{-1} diag(beta) by substitution in fp32, and
 // per chunk and value head a 19 KB block of the workspace: T (split into a bf16 high part
 // and a bf16 remainder) and P (bf16) as operand tiles, c, w, s and E_63.
@@ -101,6 +101,13 @@ __device__ __forceinline__ bool dc_cut(const uint8_t *reset, const float *g, int
     return (reset && reset[tok]) || (g && __ldg(g + tok * heads_v + h) * kLog2e < -160.0f);
 }
 
+// 16 bytes global -> shared memory, or zeros.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+
 struct DeltaPrepArgs {
     DeltaArgs d;
     int nchunks;
@@ -109,13 +116,14 @@ struct DeltaPrepArgs {
 
 // ---- preparation ---------------------------------------------------------------------
 //
-// 128 threads.  Warp w computes rows 16 w .. 16 w + 15 of K K^T and Q K^T with mma.sync
-// (64 x 64 products of a microsecond in all do not repay tensor-memory round trips), only
-// up to the diagonal, and keeps them in registers for all value heads of the key head.
-// Per value head it scales its rows of both by the decays and leaves A and P in shared
-// memory.  T is built from A in place: the inverses of the four 16 x 16 diagonal blocks by
-// substitution, one column a lane, then twice T21 = -T22 (A21 T11) for pairs of blocks in
-// packed fp32, with the intermediate product in the empty block above the diagonal.
+// 128 threads, five CTAs per SM.  Warp w computes rows 16 w .. 16 w + 15 of K K^T and
+// Q K^T with mma.sync (64 x 64 products of a microsecond in all do not repay tensor-memory
+// round trips), only up to the diagonal, scales them by the decays and leaves A and P in
+// shared memory.  T is built from A in place: the inverses of the four 16 x 16 diagonal
+// blocks by substitution, one column a lane, then twice T21 = -T22 (A21 T11) for pairs of
+// blocks in packed fp32, with the intermediate product in the empty block above the
+// diagonal.  (Value heads that share a key head repeat its two products, a tenth of the
+// work: kept in registers over the heads they cost the occupancy that hides the rest.)
 
 constexpr int kDpThreads = 128;
 constexpr int kDpRow = 136;  // elements between rows of the q and k tiles (272 bytes)
@@ -123,8 +131,8 @@ constexpr int kDpARow = 68;  // floats between rows of A
 struct DeltaPrepSmem {       // A and P take the place of the q and k tiles
     static constexpr int kK = 0, kQ = kDcChunk * kDpRow * 2;
     static constexpr int kA = 0, kP = kDcChunk * kDpARow * 4;
-    static constexpr int kScal = 2 * kQ; // per token: Gh, Gl, cut count, r, p, beta (64 floats each)
-    static constexpr int kBytes = kScal + 6 * 256 + 16;
+    static constexpr int kScal = 2 * kQ; // per token: Gh, Gl, cut count, r, p, beta, r / E, beta r E (64 floats each)
+    static constexpr int kBytes = kScal + 8 * 256 + 16;
     static_assert(kP + kDcMat <= kScal, "A and P inside the tiles");
 };
 
@@ -156,14 +164,14 @@ template <int NR> __device__ __forceinline__ void dp_rows(const float *const (&a
     }
 }
 
-__global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const DeltaPrepArgs a)
+__global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const DeltaPrepArgs a)
 {
     using Sm = DeltaPrepSmem;
     extern __shared__ __align__(128) unsigned char dp_sm[];
     const DeltaArgs &d = a.d;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int hk = int(blockIdx.x % unsigned(d.heads_k));
-    const int64_t bc = blockIdx.x / unsigned(d.heads_k);
+    const int h = int(blockIdx.x % unsigned(d.heads_v)), hk = h / d.ratio;
+    const int64_t bc = blockIdx.x / unsigned(d.heads_v);
     const int chunk = int(bc % a.nchunks);
     const int64_t b = bc / a.nchunks;
     const int64_t t0 = int64_t(chunk) * kDcChunk, tok0 = b * d.seq + t0;
@@ -173,9 +181,9 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
     float *sA = reinterpret_cast<float *>(dp_sm + Sm::kA);
     unsigned char *sPm = dp_sm + Sm::kP;
     float *sGh = reinterpret_cast<float *>(dp_sm + Sm::kScal), *sGl = sGh + 64, *sR = sGh + 192, *sP = sGh + 256,
-          *sBeta = sGh + 320;
+          *sBeta = sGh + 320, *sF = sGh + 384, *sB = sGh + 448;
     int *sN = reinterpret_cast<int *>(sGh + 128);
-    float *sRed = sGh + 384; // the first warp's totals
+    float *sRed = sGh + 512; // the first warp's totals
 
     // q and k rows, zero beyond dk and beyond the sequence
     const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(d.k) + tok0 * d.k_stride + int64_t(hk) * d.dk;
@@ -183,42 +191,53 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e = tid + kDpThreads * i, r = e >> 4, c = (e & 15) * 8;
-        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
-        if (r < n && c < d.dk) {
-            kv = __ldg(reinterpret_cast<const uint4 *>(kp + r * d.k_stride + c));
-            qv = __ldg(reinterpret_cast<const uint4 *>(qp + r * d.q_stride + c));
-        }
-        *reinterpret_cast<uint4 *>(sk + r * kDpRow + c) = kv;
-        *reinterpret_cast<uint4 *>(sq + r * kDpRow + c) = qv;
+        const bool in = r < n && c < d.dk;
+        cp_async16(sk + r * kDpRow + c, in ? kp + r * d.k_stride + c : kp, in);
+        cp_async16(sq + r * kDpRow + c, in ? qp + r * d.q_stride + c : qp, in);
     }
-    __syncthreads();
-    // lengths: thread t < 64 has k row t, the others q row t - 64
-    {
-        const __nv_bfloat16 *row = tid < 64 ? sk + tid * kDpRow : sq + (tid - 64) * kDpRow;
-        float2 s = make_float2(0.0f, 0.0f), s2 = s;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(row + 8 * c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-                (e & 1 ? s2 : s) = __ffma2_rn(x, x, e & 1 ? s2 : s);
+    // ---- decays: thread t < 64 has token t -----------------------------------------------
+    float gh = 0.0f, gl = 0.0f, be = 0.0f;
+    int cut = 0;
+    if (tid < 64) {
+        if (tid < n) {
+            const int64_t gi = (tok0 + tid) * d.heads_v + h;
+            be = d.beta ? __ldg(d.beta + gi) : 1.0f;
+            const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
+            if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
+                cut = tid > 0; // (at the first token: see above)
+            } else if (tid > 0 || chunk > 0 || d.h0) {
+                gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
+                gl = g2 - gh;
             }
         }
-        const float inv = d.l2norm ? rsqrtf((s.x + s.y) + (s2.x + s2.y) + kDeltaEps) : 1.0f;
-        if (tid < 64)
-            sR[tid] = inv;
-        else
-            sP[tid - 64] = d.scale * inv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float uh = __shfl_up_sync(0xffffffffu, gh, o), ul = __shfl_up_sync(0xffffffffu, gl, o);
+            const int uc = __shfl_up_sync(0xffffffffu, cut, o);
+            if (lane >= o) {
+                gh += uh;
+                gl += ul;
+                cut += uc;
+            }
+        }
+        if (tid == 31) {
+            sRed[0] = gh;
+            sRed[1] = gl;
+            sRed[2] = __int_as_float(cut);
+        }
+        if (tid == 0)
+            sRed[3] = t0 + kDcChunk < d.seq && dc_cut(d.reset, d.g, tok0 + kDcChunk, d.heads_v, h) ? 0.0f : 1.0f;
     }
-    // this warp's 16 rows of K K^T and Q K^T, columns 0 .. 16 warp + 15
-    float kk[8][4], qk[8][4];
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // this warp's 16 rows of K K^T and Q K^T, columns 0 .. 16 warp + 15, and the 16 x 16
+    // diagonal block of Q Q^T (for the lengths)
+    float kk[8][4], qk[8][4], qq[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            kk[i][e] = qk[i][e] = 0.0f;
+            kk[i][e] = qk[i][e] = qq[i & 1][e] = 0.0f;
     {
         const uint32_t kb = smem_u32(sk), qb = smem_u32(sq);
         // A fragments: rows 16 warp + lane % 16, columns 8 (lane / 16); B fragments (two
@@ -228,9 +247,12 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
         const int nks = (d.dk + 15) / 16;
 #pragma unroll 2
         for (int ks = 0; ks < nks; ++ks) {
-            uint32_t ak[4], aq[4];
+            uint32_t ak[4], aq[4], bq[4];
             ldmatrix_x4(ak, kb + ao + 32 * ks);
             ldmatrix_x4(aq, qb + ao + 32 * ks);
+            ldmatrix_x4(bq, qb + bo + uint32_t(16 * warp * kDpRow) * 2 + 32 * ks);
+            mma_16816(qq[0], aq, bq[0], bq[1]);
+            mma_16816(qq[1], aq, bq[2], bq[3]);
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
                 if (np <= warp) {
@@ -244,206 +266,211 @@ __global__ void __launch_bounds__(kDpThreads, 4) ss_delta_prep_kernel(const Delt
             }
         }
     }
-    for (int hh = 0; hh < d.ratio; ++hh) {
-        const int h = hk * d.ratio + hh;
-        unsigned char *blk = a.blocks + ((b * d.heads_v + h) * a.nchunks + chunk) * kDcBlockBytes;
-        // ---- decays: thread t < 64 has token t -------------------------------------------
-        float gh = 0.0f, gl = 0.0f, be = 0.0f;
-        int cut = 0;
-        if (tid < 64) {
-            if (tid < n) {
-                const int64_t gi = (tok0 + tid) * d.heads_v + h;
-                be = d.beta ? __ldg(d.beta + gi) : 1.0f;
-                const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
-                if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
-                    cut = tid > 0; // (at the first token: see above)
-                } else if (tid > 0 || chunk > 0 || d.h0) {
-                    gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
-                    gl = g2 - gh;
+    // lengths, from the diagonals: row t / 4 (+ 8 in the second tile) is in the thread
+    // whose column pair 2 (t % 4) holds it
+    {
+        const int g = lane >> 2, t2 = 2 * (lane & 3);
+        if (g == t2 || g == t2 + 1) {
+            const int e = g - t2;
+            float k0 = 0.0f, k1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w == warp) {
+                    k0 = e ? kk[2 * w][1] : kk[2 * w][0];
+                    k1 = e ? kk[2 * w + 1][3] : kk[2 * w + 1][2];
                 }
             }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float uh = __shfl_up_sync(0xffffffffu, gh, o), ul = __shfl_up_sync(0xffffffffu, gl, o);
-                const int uc = __shfl_up_sync(0xffffffffu, cut, o);
-                if (lane >= o) {
-                    gh += uh;
-                    gl += ul;
-                    cut += uc;
-                }
-            }
-            if (tid == 31) {
-                sRed[0] = gh;
-                sRed[1] = gl;
-                sRed[2] = __int_as_float(cut);
-            }
-            if (tid == 0)
-                sRed[3] = t0 + kDcChunk < d.seq && dc_cut(d.reset, d.g, tok0 + kDcChunk, d.heads_v, h) ? 0.0f : 1.0f;
+            const float q0 = e ? qq[0][1] : qq[0][0], q1 = e ? qq[1][3] : qq[1][2];
+            sR[16 * warp + g] = d.l2norm ? rsqrtf(k0 + kDeltaEps) : 1.0f;
+            sR[16 * warp + g + 8] = d.l2norm ? rsqrtf(k1 + kDeltaEps) : 1.0f;
+            sP[16 * warp + g] = d.l2norm ? d.scale * rsqrtf(q0 + kDeltaEps) : d.scale;
+            sP[16 * warp + g + 8] = d.l2norm ? d.scale * rsqrtf(q1 + kDeltaEps) : d.scale;
         }
-        __syncthreads(); // the tiles, or the previous head's T and P, have been read too
-        if (tid < 64) {
-            if (tid >= 32) {
-                gh += sRed[0];
-                gl += sRed[1];
-                cut += __float_as_int(sRed[2]);
-            }
-            sGh[tid] = gh;
-            sGl[tid] = gl;
-            sN[tid] = cut;
-            sBeta[tid] = be;
+    }
+    unsigned char *blk = a.blocks + ((b * d.heads_v + h) * a.nchunks + chunk) * kDcBlockBytes;
+    if (tid < 64) {
+        if (tid >= 32) {
+            gh += sRed[0];
+            gl += sRed[1];
+            cut += __float_as_int(sRed[2]);
         }
-        // whether E and 1 / E are in range over the whole chunk
-        const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f)));
-        if (tid < 64) {
-            const float e = cut ? 0.0f : ex2(gh + gl);
-            const float r = sR[tid];
-            reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
-            reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
-            const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
-            reinterpret_cast<float *>(blk + kDcW)[tid] =
-                hand && cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
-            if (tid == 0) {
-                reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
-                reinterpret_cast<float *>(blk + kDcE)[1] = direct ? 1.0f : 0.0f;
-            }
+        sGh[tid] = gh;
+        sGl[tid] = gl;
+        sN[tid] = cut;
+        sBeta[tid] = be;
+    }
+    // whether E and 1 / E are in range over the whole chunk
+    const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f)));
+    if (tid < 64) {
+        const float e = cut ? 0.0f : ex2(gh + gl);
+        const float r = sR[tid];
+        reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
+        // the decays factor through the chunk's start where E is in range
+        sF[tid] = r * ex2(-(gh + gl));
+        sB[tid] = be * r * e;
+        reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
+        const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
+        reinterpret_cast<float *>(blk + kDcW)[tid] =
+            hand && cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
+        if (tid == 0) {
+            reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
+            reinterpret_cast<float *>(blk + kDcE)[1] = direct ? 1.0f : 0.0f;
         }
-        // ---- A and P ---------------------------------------------------------------------
-        {
-            const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
-            float gih[2], gil[2], bi[2], pi[2];
-            int ni[2];
+    }
+    __syncthreads();
+    // ---- A and P ---------------------------------------------------------------------
+    if (!direct) {
+        const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
+        const float bi[2] = {sB[i0], sB[i0 + 8]};
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = i0 + 8 * x;
-                gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
-                bi[x] = sBeta[i] * sR[i];
-                pi[x] = sP[i];
-                if (!direct) {
-                    bi[x] *= ex2(gih[x] + gil[x]);
-                    pi[x] = 1.0f;
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                if (nt / 2 <= (warp | 1)) { // (above the diagonal: zeros of the slices of P)
-                    const int j = 8 * nt + j0;
-                    const float2 gjh = *reinterpret_cast<const float2 *>(sGh + j);
-                    const float2 gjl = *reinterpret_cast<const float2 *>(sGl + j);
-                    const int2 nj = *reinterpret_cast<const int2 *>(sN + j);
-                    const float2 rj = *reinterpret_cast<const float2 *>(sR + j);
-                    // the decays factor through the chunk's start where E is in range
-                    const float fx = rj.x * ex2(-(gjh.x + gjl.x)), fy = rj.y * ex2(-(gjh.y + gjl.y));
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int i = i0 + 8 * x;
-                        float dx = fx, dy = fy;
-                        if (direct) {
-                            dx = nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
-                            dy = nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y)) : 0.0f;
-                        }
-                        if (nt / 2 <= warp)
-                            *reinterpret_cast<float2 *>(sA + i * kDpARow + j) =
-                                make_float2(j < i ? bi[x] * dx * kk[nt][2 * x] : 0.0f,
-                                            j + 1 < i ? bi[x] * dy * kk[nt][2 * x + 1] : 0.0f);
-                        *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) =
-                            pack_bf16x2(j <= i ? pi[x] * dx * qk[nt][2 * x] : 0.0f,
-                                        j + 1 <= i ? pi[x] * dy * qk[nt][2 * x + 1] : 0.0f);
-                    }
-                }
-            }
-        }
-        __syncwarp();
-        // ---- T -------------------------------------------------------------------------------
-        // the diagonal block of this warp: lane j solves (I + A) x = e_j (both half warps the
-        // same columns)
-        {
-            float *blkA = sA + 16 * warp * (kDpARow + 1);
-            float x[16];
-            const int j = lane & 15;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x[i] = i == j ? 1.0f : 0.0f;
-#pragma unroll
-            for (int i = 1; i < 16; ++i) {
-                float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-                const float4 *row = reinterpret_cast<const float4 *>(blkA + i * kDpARow);
-#pragma unroll
-                for (int m = 0; m < (i + 3) / 4; ++m) { // A is 0 on and above the diagonal
-                    const float4 v = row[m];
-                    s0 = __ffma2_rn(make_float2(v.x, v.y), make_float2(x[4 * m], x[4 * m + 1]), s0);
-                    s1 = __ffma2_rn(make_float2(v.z, v.w), make_float2(x[4 * m + 2], x[4 * m + 3]), s1);
-                }
-                x[i] -= (s0.x + s0.y) + (s1.x + s1.y);
-            }
-            __syncwarp();
-            if (lane < 16) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    blkA[i * kDpARow + j] = x[i];
-            }
-        }
-        __syncthreads();
-        // pairs of 16 x 16 blocks: two warps each, one row of four columns a thread
-        {
-            float *base = sA + 32 * (warp >> 1) * (kDpARow + 1); // the pair's top left corner
-            const int i = (tid & 63) >> 2, c = 4 * (tid & 3);
-            float2 o[1][2];
-            const float *const a21[1] = {base + (16 + i) * kDpARow};
-            dp_rows<1>(a21, base + c, 16, o);
-            *reinterpret_cast<float4 *>(base + i * kDpARow + 16 + c) = make_float4(o[0][0].x, o[0][0].y, o[0][1].x, o[0][1].y);
-            __syncthreads();
-            const float *const t22[1] = {base + (16 + i) * kDpARow + 16};
-            dp_rows<1>(t22, base + 16 + c, 16, o);
-            *reinterpret_cast<float4 *>(base + (16 + i) * kDpARow + c) =
-                make_float4(-o[0][0].x, -o[0][0].y, -o[0][1].x, -o[0][1].y);
-        }
-        __syncthreads();
-        // the pair of 32 x 32 blocks: two rows of four columns a thread (the blocks above the
-        // diagonal 16 x 16 blocks hold leftovers and are skipped: T11's right half starts at
-        // row 16, T22's upper half ends at column 16)
-        {
-            const int right = warp >> 1; // A21 T11: the left or the right 16 columns
-            int i = (tid & 63) >> 2, c = 16 * right + 4 * (tid & 3);
-            float2 o[2][2];
-            const float *const a21[2] = {sA + (32 + i) * kDpARow + 16 * right, sA + (48 + i) * kDpARow + 16 * right};
-            dp_rows<2>(a21, sA + 16 * right * kDpARow + c, 32 - 16 * right, o);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                *reinterpret_cast<float4 *>(sA + (i + 16 * r) * kDpARow + 32 + c) =
-                    make_float4(o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y);
-            __syncthreads();
-            const int low = warp >> 1; // T22 W: the upper or the lower 16 rows
-            i = 16 * low + 2 * ((tid & 63) >> 3);
-            c = 4 * (tid & 7);
-            const float *const t22[2] = {sA + (32 + i) * kDpARow + 32, sA + (33 + i) * kDpARow + 32};
-            dp_rows<2>(t22, sA + 32 + c, 16 + 16 * low, o);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                *reinterpret_cast<float4 *>(sA + (32 + i + r) * kDpARow + c) =
-                    make_float4(-o[r][0].x, -o[r][0].y, -o[r][1].x, -o[r][1].y);
-        }
-        __syncthreads();
-        // ---- the block: T diag(beta) split, and P, in 16-byte pieces ----------------------
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            const int e = tid + kDpThreads * u; // piece: rows of 2, slices of 64, 64, 32, 32 rows
-            const int ks = e < 256 ? e >> 7 : 2 + ((e - 256) >> 6);
-            const int r = (e >> 1) & (e < 256 ? 63 : 31), i = r + (ks & 2) * 16, j = 16 * ks + 8 * (e & 1);
-            const int o = dc_elem(i, j);
-            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-            if (i >= 16 * ks) {
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt / 2 <= (warp | 1)) { // (above the diagonal: zeros of the slices of P)
+                const int j = 8 * nt + j0;
+                const float2 f = *reinterpret_cast<const float2 *>(sF + j);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float4 t = *reinterpret_cast<const float4 *>(sA + i * kDpARow + j + 4 * x);
-                    const float4 bj = *reinterpret_cast<const float4 *>(sBeta + j + 4 * x);
-                    split_bf16x2(t.x * bj.x, t.y * bj.y, hi[2 * x], lo[2 * x]);
-                    split_bf16x2(t.z * bj.z, t.w * bj.w, hi[2 * x + 1], lo[2 * x + 1]);
+                    const int i = i0 + 8 * x;
+                    float2 av = __fmul2_rn(f, make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
+                    float2 pv = __fmul2_rn(f, make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
+                    av = __fmul2_rn(make_float2(bi[x], bi[x]), av);
+                    if (nt / 2 >= warp) { // on or above the diagonal blocks
+                        av.x = j < i ? av.x : 0.0f;
+                        av.y = j + 1 < i ? av.y : 0.0f;
+                        pv.x = j <= i ? pv.x : 0.0f;
+                        pv.y = j + 1 <= i ? pv.y : 0.0f;
+                    }
+                    if (nt / 2 <= warp)
+                        *reinterpret_cast<float2 *>(sA + i * kDpARow + j) = av;
+                    *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) = pack_bf16x2(pv.x, pv.y);
                 }
             }
-            *reinterpret_cast<uint4 *>(blk + kDcThi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(blk + kDcTlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            *reinterpret_cast<uint4 *>(blk + kDcP + 16 * e) = *reinterpret_cast<const uint4 *>(sPm + 16 * e);
         }
+    } else {
+        const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
+        float gih[2], gil[2], bi[2], pi[2];
+        int ni[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = i0 + 8 * x;
+            gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
+            bi[x] = sBeta[i] * sR[i];
+            pi[x] = sP[i];
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt / 2 <= (warp | 1)) {
+                const int j = 8 * nt + j0;
+                const float2 gjh = *reinterpret_cast<const float2 *>(sGh + j);
+                const float2 gjl = *reinterpret_cast<const float2 *>(sGl + j);
+                const int2 nj = *reinterpret_cast<const int2 *>(sN + j);
+                const float2 rj = *reinterpret_cast<const float2 *>(sR + j);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = i0 + 8 * x;
+                    const float dx = j <= i && nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
+                    const float dy = j + 1 <= i && nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y))
+                                                                 : 0.0f;
+                    if (nt / 2 <= warp)
+                        *reinterpret_cast<float2 *>(sA + i * kDpARow + j) =
+                            make_float2(j < i ? bi[x] * dx * kk[nt][2 * x] : 0.0f,
+                                        j + 1 < i ? bi[x] * dy * kk[nt][2 * x + 1] : 0.0f);
+                    *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) =
+                        pack_bf16x2(pi[x] * dx * qk[nt][2 * x], pi[x] * dy * qk[nt][2 * x + 1]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    // ---- T -------------------------------------------------------------------------------
+    // the diagonal block of this warp: lane j solves (I + A) x = e_j (both half warps the
+    // same columns)
+    {
+        float *blkA = sA + 16 * warp * (kDpARow + 1);
+        float x[16];
+        const int j = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = i == j ? 1.0f : 0.0f;
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+            float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+            const float4 *row = reinterpret_cast<const float4 *>(blkA + i * kDpARow);
+#pragma unroll
+            for (int m = 0; m < (i + 3) / 4; ++m) { // A is 0 on and above the diagonal
+                const float4 v = row[m];
+                s0 = __ffma2_rn(make_float2(v.x, v.y), make_float2(x[4 * m], x[4 * m + 1]), s0);
+                s1 = __ffma2_rn(make_float2(v.z, v.w), make_float2(x[4 * m + 2], x[4 * m + 3]), s1);
+            }
+            x[i] -= (s0.x + s0.y) + (s1.x + s1.y);
+        }
+        __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                blkA[i * kDpARow + j] = x[i];
+        }
+    }
+    __syncthreads();
+    // pairs of 16 x 16 blocks: two warps each, one row of four columns a thread
+    {
+        float *base = sA + 32 * (warp >> 1) * (kDpARow + 1); // the pair's top left corner
+        const int i = (tid & 63) >> 2, c = 4 * (tid & 3);
+        float2 o[1][2];
+        const float *const a21[1] = {base + (16 + i) * kDpARow};
+        dp_rows<1>(a21, base + c, 16, o);
+        *reinterpret_cast<float4 *>(base + i * kDpARow + 16 + c) = make_float4(o[0][0].x, o[0][0].y, o[0][1].x, o[0][1].y);
+        __syncthreads();
+        const float *const t22[1] = {base + (16 + i) * kDpARow + 16};
+        dp_rows<1>(t22, base + 16 + c, 16, o);
+        *reinterpret_cast<float4 *>(base + (16 + i) * kDpARow + c) =
+            make_float4(-o[0][0].x, -o[0][0].y, -o[0][1].x, -o[0][1].y);
+    }
+    __syncthreads();
+    // the pair of 32 x 32 blocks: two rows of four columns a thread (the blocks above the
+    // diagonal 16 x 16 blocks hold leftovers and are skipped: T11's right half starts at
+    // row 16, T22's upper half ends at column 16)
+    {
+        const int right = warp >> 1; // A21 T11: the left or the right 16 columns
+        int i = (tid & 63) >> 2, c = 16 * right + 4 * (tid & 3);
+        float2 o[2][2];
+        const float *const a21[2] = {sA + (32 + i) * kDpARow + 16 * right, sA + (48 + i) * kDpARow + 16 * right};
+        dp_rows<2>(a21, sA + 16 * right * kDpARow + c, 32 - 16 * right, o);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4 *>(sA + (i + 16 * r) * kDpARow + 32 + c) =
+                make_float4(o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y);
+        __syncthreads();
+        const int low = warp >> 1; // T22 W: the upper or the lower 16 rows
+        i = 16 * low + 2 * ((tid & 63) >> 3);
+        c = 4 * (tid & 7);
+        const float *const t22[2] = {sA + (32 + i) * kDpARow + 32, sA + (33 + i) * kDpARow + 32};
+        dp_rows<2>(t22, sA + 32 + c, 16 + 16 * low, o);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4 *>(sA + (32 + i + r) * kDpARow + c) =
+                make_float4(-o[r][0].x, -o[r][0].y, -o[r][1].x, -o[r][1].y);
+    }
+    __syncthreads();
+    // ---- the block: T diag(beta) split, and P, in 16-byte pieces ----------------------
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int e = tid + kDpThreads * u; // piece: rows of 2, slices of 64, 64, 32, 32 rows
+        const int ks = e < 256 ? e >> 7 : 2 + ((e - 256) >> 6);
+        const int r = (e >> 1) & (e < 256 ? 63 : 31), i = r + (ks & 2) * 16, j = 16 * ks + 8 * (e & 1);
+        const int o = dc_elem(i, j);
+        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+        if (i >= 16 * ks) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 t = *reinterpret_cast<const float4 *>(sA + i * kDpARow + j + 4 * x);
+                const float4 bj = *reinterpret_cast<const float4 *>(sBeta + j + 4 * x);
+                split_bf16x2(t.x * bj.x, t.y * bj.y, hi[2 * x], lo[2 * x]);
+                split_bf16x2(t.z * bj.z, t.w * bj.w, hi[2 * x + 1], lo[2 * x + 1]);
+            }
+        }
+        *reinterpret_cast<uint4 *>(blk + kDcThi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(blk + kDcTlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(blk + kDcP + 16 * e) = *reinterpret_cast<const uint4 *>(sPm + 16 * e);
     }
 }
 
@@ -478,18 +505,19 @@ struct DwSmem { // from a 1024-byte aligned base
 static_assert(DwSmem::kBytes <= 113 * 1024, "shared memory of the walk");
 
 struct DeltaWalkArgs {
-    int64_t batch, seq;
-    int heads_v, ratio, dk, dv;
+    int64_t batch;
+    int seq, heads_v, ratio, dk, dv;
     int nchunks, col_tiles, nks;  // nks: 16-key slices of the state
     const unsigned char *blocks;
     const float *h0;              // nullable
     const float *g;               // nullable; g and reset for the first token
     const uint8_t *reset;         // nullable
+    __nv_bfloat16 *y;
     float *final_state;           // nullable
 };
 
 struct DeltaWalkMaps {
-    CUtensorMap q, k, v, y; // 4-D (d, head, token, batch); boxes (64, 1, 64, 1), y (16 MT, 1, 32, 1)
+    CUtensorMap q, k, v; // 4-D (d, head, token, batch), boxes (64, 1, 64, 1)
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
@@ -534,16 +562,6 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// Tile store, shared memory -> global, through a tensor map (what lies beyond the tensor
-// is left out).
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2,
-                                             int32_t c3)
-{
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
-                 : "memory");
-}
 // The element-wise steps hold tiles of 16 lanes as the warp-wide fragments that
 // tcgen05.ld.16x256b, tcgen05.st.16x128b, ldmatrix and stmatrix share: thread t has rows
 // t / 4 and t / 4 + 8 (x = 0, 1), and of every 8 columns the pair 2 (t % 4), + 1.
@@ -841,6 +859,10 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         const uint32_t v_base = s_base + DwSmem::kV + (q4 >> 1) * 8192; // the tile of this warp's values
         unsigned char *ytile = sm + DwSmem::kY + warp * (1024 * MT);
         const uint32_t y_base = smem_u32(ytile);
+        // this lane's 16 bytes of the tile's first rows; rows 32 >> MT further on, ystep more
+        const int64_t ystep = int64_t(32 >> MT) * a.heads_v * a.dv;
+        __nv_bfloat16 *yp = a.y + ((b * a.seq + 32 * cg + (lane >> MT)) * a.heads_v + h) * a.dv + n0 + row0 +
+                            8 * (lane & (2 * MT - 1));
         for (int c = 0; c < a.nchunks; ++c) {
             const int st = c & 1;
             const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
@@ -913,10 +935,6 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
             }
             tmem_st_wait();
-            // (before the arrival that the products of this chunk wait for: the store of the
-            // last outputs has read this warp's tile)
-            if (lane == 0)
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             arrive(arr_r);
             // ---- U^T rounded, and w o U over it -----------------------------------------------
             if (!wait(bar_u, ph)) {
@@ -963,9 +981,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int k = 2 * j + i;
-                        float2 sv = make_float2(1.0f, 1.0f);
-                        if (em.y == 0.0f)
-                            sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
+                        float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
+                        sv.x = em.y == 0.0f ? sv.x : 1.0f;
+                        sv.y = em.y == 0.0f ? sv.y : 1.0f;
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * k + x));
@@ -978,12 +996,20 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     stmatrix_x4_trans(y_base + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1)), o);
                 }
             }
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                if (n0 + row0 < a.dv && int64_t(c) * kDcChunk + 32 * cg < a.seq)
-                    tma_store_4d(&maps.y, ytile, n0 + row0, h, c * kDcChunk + 32 * cg, int32_t(b));
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            // back as rows of the tile, 16 bytes a lane (a TMA store per warp and the proxy fence
+            // before it took three times as long)
+            {
+                const int t = ln >> MT, ch = ln & (2 * MT - 1); // (the swizzle repeats every 8 rows)
+                const unsigned char *src = ytile + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1));
+                const int left = a.seq - c * kDcChunk - 32 * cg - t;
+                const bool in = n0 + row0 + 8 * ch < a.dv; // (dv is a multiple of 8)
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+                    if (in && left > (32 >> MT) * i)
+                        *reinterpret_cast<uint4 *>(yp + i * ystep) =
+                            *reinterpret_cast<const uint4 *>(src + 32 * MT * (32 >> MT) * i);
+                yp += (2 << MT) * ystep;
             }
             // ---- H = E_63 H + dH -------------------------------------------------------------
             if (!wait(bar_dh + cg, ph)) {
@@ -1011,8 +1037,6 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             tmem_st_wait();
             arrive(arr_h);
         }
-        if (lane == 0) // the tile must not go away under a store
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         if (ok && a.final_state) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
