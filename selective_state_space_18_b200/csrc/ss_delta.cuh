@@ -35,15 +35,15 @@ struct DeltaArgs {
 //
 // A CTA owns one (batch row, value head) and 16 of its value columns: columns of the
 // state never meet.  Four consumer warps hold the state in registers, a column's dk rows
-// over 8 lanes; two producer warps stage the next 16 tokens (q and k in fp32, normalised
-// and scaled, zero-padded to the kernel's dk; v; the decay, beta and q . k) while the
-// consumers walk the current ones.  Per token a consumer lane reads its 4 R4 rows of k
+// over 8 lanes; eight producer warps stage the next 16 tokens, two each (q and k in fp32,
+// normalised and scaled, zero-padded to the kernel's dk; v; the decay, beta and q . k),
+// while the consumers walk the current ones.  Per token a consumer lane reads its 4 R4 rows of k
 // and q with 16-byte loads (four columns of a warp share each), and the two dot products
 // are reduced over the 8 lanes together.  What bounds it is the latency of that chain,
 // token after token, so it serves fp32 storage, key sizes the chunked form does not take
 // and prompts of a few tokens; all its arithmetic is fp32.
 
-constexpr int kDrCols = 16, kDrTok = 16, kDrConsumers = 128, kDrProducers = 64;
+constexpr int kDrCols = 16, kDrTok = 16, kDrConsumers = 128, kDrProducers = 256;
 constexpr int kDrThreads = kDrConsumers + kDrProducers;
 
 template <int R4> struct DeltaRecSmem { // floats of one staging buffer
@@ -67,30 +67,40 @@ __global__ void __launch_bounds__(kDrThreads) ss_delta_rec_kernel(const DeltaArg
     const int64_t tok0 = b * a.seq; // first token of this batch row
     const int64_t ntiles = (a.seq + kDrTok - 1) / kDrTok;
 
-    // producer warp w (0 or 1) stages tokens w, w + 2, ... of a tile
+    // producer warp w stages tokens w and w + 8 of a tile, the loads of both in flight together
     auto stage = [&](int64_t tile, float *buf) {
+        constexpr int kPer = kDrTok / (kDrProducers / 32);
         const int w = (tid - kDrConsumers) >> 5;
-#pragma unroll 2
-        for (int t = w; t < kDrTok; t += 2) {
-            const int64_t pos = tile * kDrTok + t;
-            if (pos >= a.seq)
-                break;
-            const int64_t tok = tok0 + pos;
+        float q[kPer][R4], k[kPer][R4], v[kPer], g[kPer], be[kPer];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int64_t pos = tile * kDrTok + w + u * (kDrProducers / 32);
+            const bool in = pos < a.seq;
+            const int64_t tok = tok0 + (in ? pos : 0), gi = tok * a.heads_v + h;
             const T *qp = static_cast<const T *>(a.q) + tok * a.q_stride + int64_t(hk) * a.dk;
             const T *kp = static_cast<const T *>(a.k) + tok * a.k_stride + int64_t(hk) * a.dk;
-            const T *vp = static_cast<const T *>(a.v) + tok * a.v_stride + int64_t(h) * a.dv;
-            float q[R4], k[R4], qq = 0.0f, kk = 0.0f, qk = 0.0f;
+            const T *vp = static_cast<const T *>(a.v) + tok * a.v_stride + int64_t(h) * a.dv + c0;
 #pragma unroll
             for (int j = 0; j < R4; ++j) {
                 const int i = lane + 32 * j;
-                q[j] = i < a.dk ? Elem<T>::load(qp + i) : 0.0f;
-                k[j] = i < a.dk ? Elem<T>::load(kp + i) : 0.0f;
+                q[u][j] = in && i < a.dk ? Elem<T>::load(qp + i) : 0.0f;
+                k[u][j] = in && i < a.dk ? Elem<T>::load(kp + i) : 0.0f;
             }
+            v[u] = in && lane < kDrCols && c0 + lane < a.dv ? Elem<T>::load(vp + lane) : 0.0f;
+            g[u] = a.g ? __ldg(a.g + gi) : 0.0f;
+            be[u] = a.beta ? __ldg(a.beta + gi) : 1.0f;
+            if (a.reset && a.reset[tok])
+                g[u] = -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int t = w + u * (kDrProducers / 32);
+            float qq = 0.0f, kk = 0.0f, qk = 0.0f;
 #pragma unroll
             for (int j = 0; j < R4; ++j) {
-                qq = fmaf(q[j], q[j], qq);
-                kk = fmaf(k[j], k[j], kk);
-                qk = fmaf(q[j], k[j], qk);
+                qq = fmaf(q[u][j], q[u][j], qq);
+                kk = fmaf(k[u][j], k[u][j], kk);
+                qk = fmaf(q[u][j], k[u][j], qk);
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
@@ -105,18 +115,13 @@ __global__ void __launch_bounds__(kDrThreads) ss_delta_rec_kernel(const DeltaArg
             }
 #pragma unroll
             for (int j = 0; j < R4; ++j) {
-                buf[Sm::kQ + t * Sm::kDk + lane + 32 * j] = rq * q[j];
-                buf[Sm::kK + t * Sm::kDk + lane + 32 * j] = rk * k[j];
+                buf[Sm::kQ + t * Sm::kDk + lane + 32 * j] = rq * q[u][j];
+                buf[Sm::kK + t * Sm::kDk + lane + 32 * j] = rk * k[u][j];
             }
             if (lane < kDrCols)
-                buf[Sm::kV + t * kDrCols + lane] = c0 + lane < a.dv ? Elem<T>::load(vp + c0 + lane) : 0.0f;
-            if (lane == 0) {
-                const int64_t gi = tok * a.heads_v + h;
-                const bool cut = a.reset && a.reset[tok];
-                buf[Sm::kS + 4 * t] = cut ? 0.0f : (a.g ? expf(__ldg(a.g + gi)) : 1.0f);
-                buf[Sm::kS + 4 * t + 1] = a.beta ? __ldg(a.beta + gi) : 1.0f;
-                buf[Sm::kS + 4 * t + 2] = qk * rq * rk;
-            }
+                buf[Sm::kV + t * kDrCols + lane] = v[u];
+            if (lane == 0)
+                *reinterpret_cast<float4 *>(buf + Sm::kS + 4 * t) = make_float4(expf(g[u]), be[u], qk * rq * rk, 0.0f);
         }
     };
 
@@ -154,6 +159,11 @@ __global__ void __launch_bounds__(kDrThreads) ss_delta_rec_kernel(const DeltaArg
                 const float4 *q4 = reinterpret_cast<const float4 *>(buf + Sm::kQ + t * Sm::kDk) + p;
                 const float4 sc = *reinterpret_cast<const float4 *>(buf + Sm::kS + 4 * t);
                 const float v = buf[Sm::kV + t * kDrCols + col];
+                if (sc.x == 0.0f) { // a decay of 0 discards the state, whatever it holds
+#pragma unroll
+                    for (int i = 0; i < 4 * R4; ++i)
+                        S[i] = 0.0f;
+                }
                 float4 k[R4];
                 float ks0 = 0.0f, ks1 = 0.0f, qs0 = 0.0f, qs1 = 0.0f;
 #pragma unroll
@@ -175,16 +185,15 @@ __global__ void __launch_bounds__(kDrThreads) ss_delta_rec_kernel(const DeltaArg
                     ks += __shfl_xor_sync(0xffffffffu, ks, o);
                     qs += __shfl_xor_sync(0xffffffffu, qs, o);
                 }
-                // a decay of 0 discards the state, whatever it holds
                 const float d = sc.x;
-                const float u = sc.y * (v - (d == 0.0f ? 0.0f : d * ks));
-                const float y = fmaf(sc.z, u, d == 0.0f ? 0.0f : d * qs);
+                const float u = sc.y * fmaf(-d, ks, v);
+                const float y = fmaf(sc.z, u, d * qs);
 #pragma unroll
                 for (int j = 0; j < R4; ++j) {
                     const float kv[4] = {k[j].x, k[j].y, k[j].z, k[j].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        S[4 * j + e] = fmaf(kv[e], u, d == 0.0f ? 0.0f : d * S[4 * j + e]);
+                        S[4 * j + e] = fmaf(kv[e], u, d * S[4 * j + e]);
                 }
                 if (p == 0 && live)
                     Elem<T>::store(yp, y);
@@ -227,51 +236,62 @@ struct DeltaUpdateArgs {
 
 constexpr int kDuThreads = 128, kDuCols = 32;
 
+// Six CTAs per SM (for dk up to 128) with packed fp32 arithmetic: 162 us for 256 x 32
+// states of 128 x 128, the rate of a plain copy; 194 us with scalar arithmetic and four.
+// (Tiles of 64 or 128 columns, 171 and 186 us: fewer CTAs whose phases overlap.)
 // J: row groups of 16 (dk <= 16 J).  VEC: dv a multiple of 4 and a 16-byte aligned state.
-template <typename T, int J, bool VEC>
-__global__ void __launch_bounds__(kDuThreads) ss_delta_update_kernel(const DeltaUpdateArgs a)
+// FULL: dk = 16 J and dv a multiple of 32 as well, so that nothing is guarded (176 us with
+// the guards).
+template <typename T, int J, bool VEC, bool FULL>
+__global__ void __launch_bounds__(kDuThreads, J <= 8 ? 6 : 3) ss_delta_update_kernel(const DeltaUpdateArgs a)
 {
+    static_assert(VEC || !FULL, "full tiles are read as vectors");
     __shared__ float red[4][8][12];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c4 = tid & 7, r = tid >> 3;
-    const int64_t bh = blockIdx.x / a.col_tiles;
-    const int c = int(blockIdx.x % a.col_tiles) * kDuCols + 4 * c4;
+    const int64_t bh = blockIdx.x / unsigned(a.col_tiles);
+    const int c = int(blockIdx.x % unsigned(a.col_tiles)) * kDuCols + 4 * c4;
     const int64_t b = bh / a.heads_v;
     const int h = int(bh % a.heads_v), hk = h / a.ratio;
     float *sp = a.state + bh * a.dk * a.dv + c;
-    float S[J][4];
+    float2 S[J][2]; // columns c, c + 1 and c + 2, c + 3
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int row = r + 16 * j;
         if constexpr (VEC) {
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (row < a.dk && c < a.dv)
+            if (FULL || (row < a.dk && c < a.dv))
                 v = __ldcs(reinterpret_cast<const float4 *>(sp + int64_t(row) * a.dv));
-            S[j][0] = v.x, S[j][1] = v.y, S[j][2] = v.z, S[j][3] = v.w;
+            S[j][0] = make_float2(v.x, v.y), S[j][1] = make_float2(v.z, v.w);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                S[j][e] = row < a.dk && c + e < a.dv ? sp[int64_t(row) * a.dv + e] : 0.0f;
+            for (int e = 0; e < 2; ++e) {
+                S[j][e].x = row < a.dk && c + 2 * e < a.dv ? sp[int64_t(row) * a.dv + 2 * e] : 0.0f;
+                S[j][e].y = row < a.dk && c + 2 * e + 1 < a.dv ? sp[int64_t(row) * a.dv + 2 * e + 1] : 0.0f;
+            }
         }
     }
     const T *qp = static_cast<const T *>(a.q) + b * a.q_stride + int64_t(hk) * a.dk;
     const T *kp = static_cast<const T *>(a.k) + b * a.k_stride + int64_t(hk) * a.dk;
     float k[J];
-    float s[11] = {}; // k . S and q . S of 4 columns, k . k, q . q, q . k
+    float2 ks[2] = {}, qs[2] = {};
+    float kk = 0.0f, qq = 0.0f, qdk = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int row = r + 16 * j;
-        k[j] = row < a.dk ? Elem<T>::load(kp + row) : 0.0f;
-        const float q = row < a.dk ? Elem<T>::load(qp + row) : 0.0f;
+        k[j] = FULL || row < a.dk ? Elem<T>::load(kp + row) : 0.0f;
+        const float q = FULL || row < a.dk ? Elem<T>::load(qp + row) : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[e] = fmaf(k[j], S[j][e], s[e]);
-            s[4 + e] = fmaf(q, S[j][e], s[4 + e]);
+        for (int e = 0; e < 2; ++e) {
+            ks[e] = __ffma2_rn(make_float2(k[j], k[j]), S[j][e], ks[e]);
+            qs[e] = __ffma2_rn(make_float2(q, q), S[j][e], qs[e]);
         }
-        s[8] = fmaf(k[j], k[j], s[8]);
-        s[9] = fmaf(q, q, s[9]);
-        s[10] = fmaf(q, k[j], s[10]);
+        kk = fmaf(k[j], k[j], kk);
+        qq = fmaf(q, q, qq);
+        qdk = fmaf(q, k[j], qdk);
     }
+    // k . S and q . S of 4 columns, k . k, q . q, q . k
+    float s[11] = {ks[0].x, ks[0].y, ks[1].x, ks[1].y, qs[0].x, qs[0].y, qs[1].x, qs[1].y, kk, qq, qdk};
 #pragma unroll
     for (int i = 0; i < 11; ++i) {
         s[i] += __shfl_xor_sync(0xffffffffu, s[i], 8);
@@ -294,32 +314,45 @@ __global__ void __launch_bounds__(kDuThreads) ss_delta_update_kernel(const Delta
     const float qk = s[10] * rq * rk;
     const T *vp = static_cast<const T *>(a.v) + b * a.v_stride + int64_t(h) * a.dv + c;
     T *yp = static_cast<T *>(a.y) + (b * a.heads_v + h) * a.dv + c;
+    if (d == 0.0f) { // a decay of 0 discards the state, whatever it holds
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            S[j][0] = S[j][1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[i] = 0.0f;
+    }
     float u[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float v = c + e < a.dv ? Elem<T>::load(vp + e) : 0.0f;
-        u[e] = be * (v - (d == 0.0f ? 0.0f : d * rk * s[e]));
-        if (r == 0 && c + e < a.dv)
-            Elem<T>::store(yp + e, fmaf(qk, u[e], d == 0.0f ? 0.0f : d * rq * s[4 + e]));
+        const float v = FULL || c + e < a.dv ? Elem<T>::load(vp + e) : 0.0f;
+        u[e] = be * fmaf(-d * rk, s[e], v);
+        if (r == 0 && (FULL || c + e < a.dv))
+            Elem<T>::store(yp + e, fmaf(qk, u[e], d * rq * s[4 + e]));
         u[e] *= rk;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int row = r + 16 * j;
-        if (row >= a.dk)
+        if (!FULL && row >= a.dk)
             break;
-        float o[4];
+        float2 o[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] = fmaf(k[j], u[e], d == 0.0f ? 0.0f : d * S[j][e]);
+        for (int e = 0; e < 2; ++e) {
+            o[e] = __ffma2_rn(make_float2(k[j], k[j]), make_float2(u[2 * e], u[2 * e + 1]),
+                              __fmul2_rn(make_float2(d, d), S[j][e]));
+        }
         if constexpr (VEC) {
-            if (c < a.dv)
-                __stcs(reinterpret_cast<float4 *>(sp + int64_t(row) * a.dv), make_float4(o[0], o[1], o[2], o[3]));
+            if (FULL || c < a.dv)
+                __stcs(reinterpret_cast<float4 *>(sp + int64_t(row) * a.dv), make_float4(o[0].x, o[0].y, o[1].x, o[1].y));
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < a.dv)
-                    sp[int64_t(row) * a.dv + e] = o[e];
+            for (int e = 0; e < 2; ++e) {
+                if (c + 2 * e < a.dv)
+                    sp[int64_t(row) * a.dv + 2 * e] = o[e].x;
+                if (c + 2 * e + 1 < a.dv)
+                    sp[int64_t(row) * a.dv + 2 * e + 1] = o[e].y;
+            }
         }
     }
 }

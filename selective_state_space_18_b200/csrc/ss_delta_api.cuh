@@ -169,10 +169,13 @@ template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cuda
     int64_t grid = 0;
     if (!mul_ok(a.batch * a.heads_v, a.col_tiles, &grid) || grid > 0x7fffffffLL)
         return SS_ERR_SHAPE;
-    if (a.dv % 4 == 0 && aligned(a.state, 16))
-        ss::ss_delta_update_kernel<T, J, true><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
+    const bool vec = a.dv % 4 == 0 && aligned(a.state, 16);
+    if (vec && a.dk == 16 * J && a.dv % ss::kDuCols == 0)
+        ss::ss_delta_update_kernel<T, J, true, true><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
+    else if (vec)
+        ss::ss_delta_update_kernel<T, J, true, false><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
     else
-        ss::ss_delta_update_kernel<T, J, false><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
+        ss::ss_delta_update_kernel<T, J, false, false><<<unsigned(grid), ss::kDuThreads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -190,28 +193,33 @@ template <typename T, int VEC, int NV, bool CTA> int launch_group_norm(const ss:
         return SS_ERR_CUDA;
     const int64_t per_cta = CTA ? 1 : ss::kGnThreads >> a.team_log2;
     const int64_t blocks = (a.rows * a.groups + per_cta - 1) / per_cta;
-    const int64_t most = int64_t(sms) * 32;
+    const int64_t most = int64_t(sms) * 16;
     ss::ss_group_norm_kernel<T, VEC, NV, CTA>
         <<<unsigned(blocks < most ? blocks : most), ss::kGnThreads, 0, s>>>(a);
     return launch_status();
 }
 
-// Teams: the fewest lanes of a warp that hold a group in one vector each; up to eight
-// vectors a lane for a whole warp; beyond that the CTA.
+// Teams: the fewest lanes of a warp that hold a group in `kMost` vectors each, or a warp
+// with up to eight; beyond that the CTA.  kMost 2 for 16-byte vectors (16384 x 32 groups
+// of 128 bf16 with a gate: 72 us against 78-90 with one vector a lane), 8 for single
+// elements (16384 x 5 groups of 83: 27 us against 31 with a whole warp).
 template <typename T, int VEC> int dispatch_group_norm(ss::GroupNormArgs &a, cudaStream_t s)
 {
+    constexpr int kMost = VEC == 1 ? 8 : 2;
     const int vecs = (a.size + VEC - 1) / VEC;
     a.team_log2 = 0;
-    while (a.team_log2 < 5 && (1 << a.team_log2) < vecs)
+    while (a.team_log2 < 5 && (kMost << a.team_log2) < vecs)
         ++a.team_log2;
-    if (vecs <= 32)
-        return launch_group_norm<T, VEC, 1, false>(a, s);
-    if (vecs <= 64)
-        return launch_group_norm<T, VEC, 2, false>(a, s);
-    if (vecs <= 128)
-        return launch_group_norm<T, VEC, 4, false>(a, s);
-    if (vecs <= 256)
-        return launch_group_norm<T, VEC, 8, false>(a, s);
+    switch ((vecs + (1 << a.team_log2) - 1) >> a.team_log2) {
+    case 1: return launch_group_norm<T, VEC, 1, false>(a, s);
+    case 2: return launch_group_norm<T, VEC, 2, false>(a, s);
+    case 3: return launch_group_norm<T, VEC, 3, false>(a, s);
+    case 4: return launch_group_norm<T, VEC, 4, false>(a, s);
+    case 5: return launch_group_norm<T, VEC, 5, false>(a, s);
+    case 6: return launch_group_norm<T, VEC, 6, false>(a, s);
+    case 7:
+    case 8: return launch_group_norm<T, VEC, 8, false>(a, s);
+    }
     if (vecs <= 4 * ss::kGnThreads)
         return launch_group_norm<T, VEC, 4, true>(a, s);
     if constexpr (VEC == 1) {

@@ -10,8 +10,8 @@
 // distances from it (no difference of large sums).
 //
 // Bound by HBM: x and the gate are read once and y is written once.  A group is held in
-// the registers of a team of lanes: 2^k lanes of a warp when it fits into 32 lanes of NV
-// vectors, a whole CTA of 256 threads otherwise.  Vectors are 16 bytes where the group
+// the registers of a team of lanes: 2^k lanes of a warp when it fits into 32 lanes of up
+// to eight vectors, a whole CTA of 256 threads otherwise.  Vectors are 16 bytes where the group
 // size and every row allow it (VEC elements), single elements elsewhere.
 #pragma once
 
@@ -105,110 +105,166 @@ template <bool CTA> __device__ __forceinline__ float gn_sum(float v, int team_lo
     }
 }
 
-// One group per team and turn; teams take groups grid-strided.
-template <typename T, int VEC, int NV, bool CTA>
-__global__ void __launch_bounds__(kGnThreads) ss_group_norm_kernel(const GroupNormArgs a)
+// silu of a pair: v / (1 + 2^(-v log2 e)), with the reciprocal of the hardware (1 ulp; of
+// infinity it is 0, so large negative v give -0).
+__device__ __forceinline__ float2 gn_silu2(float2 v)
 {
+    const float2 t = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.0f, 1.0f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    return __fmul2_rn(v, r);
+}
+
+// CTAs per SM to ask for, by the elements a lane holds: the loads in flight are what hides
+// the memory's latency, and a lane has one vector per 8 (or 4) of its elements in flight.
+__host__ __device__ constexpr int gn_min_ctas(int elements)
+{
+    return elements <= 8 ? 6 : elements <= 16 ? 4 : elements <= 24 ? 3 : elements <= 40 ? 2 : 1;
+}
+
+// One group per team and turn; teams take groups grid-strided.  A lane's elements are held
+// and worked on as pairs (packed fp32 arithmetic: two elements an instruction); the
+// instructions per element are what a group of many small rows is bound by.
+template <typename T, int VEC, int NV, bool CTA>
+__global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_norm_kernel(const GroupNormArgs a)
+{
+    constexpr int kE = NV * VEC, kP = (kE + 1) / 2; // elements and pairs of a lane
     __shared__ float red[kGnThreads / 32];
     const int team = CTA ? kGnThreads : 1 << a.team_log2;
     const int per_cta = kGnThreads / team, lane = threadIdx.x & (team - 1);
     const int64_t total = a.rows * a.groups;
     const int64_t step = int64_t(gridDim.x) * per_cta;
+    // (row, group) of the team's item, advanced without divisions
+    const int64_t row_step = step / a.groups;
+    const int grp_step = int(step - row_step * a.groups);
+    int64_t item = int64_t(blockIdx.x) * per_cta + threadIdx.x / team;
+    int64_t row = item / a.groups;
+    int grp = int(item - row * a.groups);
+    const bool gated = a.gate != nullptr, gate_first = gated && (a.mode & kGnGateFirst);
+    const int c0 = VEC * lane; // this lane's first element; its vectors are VEC * team apart
     // every lane of a warp makes the same number of turns (the sums are warp-collective)
     for (int64_t first = int64_t(blockIdx.x) * per_cta; first < total; first += step) {
-        const int64_t item = first + threadIdx.x / team;
-        const bool live = item < total;
-        const int64_t row = live ? item / a.groups : 0;
-        const int grp = live ? int(item - row * a.groups) : 0;
-        const T *xp = static_cast<const T *>(a.x) + row * a.x_stride + int64_t(grp) * a.size;
-        const T *zp = a.gate ? static_cast<const T *>(a.gate) + row * a.gate_stride + int64_t(grp) * a.size : nullptr;
-        float x[NV][VEC];
-        GnVec<T, VEC> zv[NV];
+        const int size = item < total ? a.size : 0; // 0: nothing to do this turn
+        const int64_t at = row * a.x_stride + int64_t(grp) * a.size;
+        GnVec<T, VEC> xv[NV], zv[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = VEC * (lane + team * i);
-            GnVec<T, VEC> xv;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                x[i][e] = 0.0f;
-            if (live && c < a.size) {
-                xv.load(xp + c);
-                if (zp)
-                    zv[i].load(zp + c);
-                xv.get(x[i]);
-            }
-        }
-        if (zp && (a.mode & kGnGateFirst)) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (live && VEC * (lane + team * i) < a.size) {
-                    float z[VEC];
-                    zv[i].get(z);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        x[i][e] *= silu(z[e]);
-                }
-            }
-        }
-        float mean = 0.0f;
-        if (a.mode & kGnCenter) {
-            float s = 0.0f;
+        for (int i = 0; i < NV; ++i)
+            if (c0 + VEC * team * i < size)
+                xv[i].load(static_cast<const T *>(a.x) + at + c0 + VEC * team * i);
+        if (gated) {
+            const int64_t zat = row * a.gate_stride + int64_t(grp) * a.size;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
+                if (c0 + VEC * team * i < size)
+                    zv[i].load(static_cast<const T *>(a.gate) + zat + c0 + VEC * team * i);
+        }
+        float2 x[kP];
+        auto unpack = [&](const GnVec<T, VEC> (&raw)[NV], float2 (&f)[kP]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float v[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    s += x[i][e];
-            mean = gn_sum<CTA>(s, a.team_log2, red) * a.inv_size;
+                    v[e] = 0.0f;
+                if (c0 + VEC * team * i < size)
+                    raw[i].get(v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    ((VEC * i + e) & 1 ? f[(VEC * i + e) / 2].y : f[(VEC * i + e) / 2].x) = v[e];
+            }
+            if constexpr (kE & 1)
+                f[kP - 1].y = 0.0f;
+        };
+        unpack(xv, x);
+        if (gate_first) {
+            float2 z[kP];
+            unpack(zv, z);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                x[p] = __fmul2_rn(x[p], gn_silu2(z[p]));
         }
-        float s2 = 0.0f;
+        if (a.mode & kGnCenter) {
+            float2 s = x[0];
+#pragma unroll
+            for (int p = 1; p < kP; ++p)
+                s = __fadd2_rn(s, x[p]);
+            const float mean = gn_sum<CTA>(s.x + s.y, a.team_log2, red) * a.inv_size;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) { // (elements beyond the group stay 0)
+                float &f = e & 1 ? x[e / 2].y : x[e / 2].x;
+                f = c0 + VEC * team * (e / VEC) < size ? f - mean : 0.0f;
+            }
+        }
+        float2 s2 = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+        for (int p = 1; p < kP; ++p)
+            s2 = __ffma2_rn(x[p], x[p], s2);
+        const float rs = rsqrtf(gn_sum<CTA>(s2.x + s2.y, a.team_log2, red) * a.inv_size + a.eps);
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+            x[p] = __fmul2_rn(x[p], make_float2(rs, rs));
+        const int pofs = ((a.mode & kGnShared) ? 0 : grp * a.size) + c0;
+        auto params = [&](const float *src, float2 (&f)[kP]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float v[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    v[e] = 0.0f;
+                if (c0 + VEC * team * i < size)
+                    gn_params<VEC>(src, pofs + VEC * team * i, v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    ((VEC * i + e) & 1 ? f[(VEC * i + e) / 2].y : f[(VEC * i + e) / 2].x) = v[e];
+            }
+            if constexpr (kE & 1)
+                f[kP - 1].y = 0.0f;
+        };
+        if (a.weight) {
+            float2 w[kP];
+            params(a.weight, w);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                x[p] = __fmul2_rn(x[p], w[p]);
+        }
+        if (a.bias) {
+            float2 w[kP];
+            params(a.bias, w);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                x[p] = __fadd2_rn(x[p], w[p]);
+        }
+        if (a.mode & kGnSilu) {
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                x[p] = gn_silu2(x[p]);
+        }
+        if (gated && !gate_first) {
+            float2 z[kP];
+            unpack(zv, z);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                x[p] = __fmul2_rn(x[p], gn_silu2(z[p]));
+        }
+        T *yp = static_cast<T *>(a.y) + (row * a.groups + grp) * a.size + c0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (VEC * (lane + team * i) < a.size) {
+            if (c0 + VEC * team * i < size) {
+                float o[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    x[i][e] -= mean;
-                    s2 = fmaf(x[i][e], x[i][e], s2);
-                }
+                for (int e = 0; e < VEC; ++e)
+                    o[e] = (VEC * i + e) & 1 ? x[(VEC * i + e) / 2].y : x[(VEC * i + e) / 2].x;
+                GnVec<T, VEC>::store(yp + VEC * team * i, o);
             }
         }
-        const float rs = rsqrtf(gn_sum<CTA>(s2, a.team_log2, red) * a.inv_size + a.eps);
-        if (!live)
-            continue;
-        T *yp = static_cast<T *>(a.y) + (row * a.groups + grp) * a.size;
-        const int pofs = (a.mode & kGnShared) ? 0 : grp * a.size;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = VEC * (lane + team * i);
-            if (c >= a.size)
-                break;
-            float o[VEC], w[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                o[e] = x[i][e] * rs;
-            if (a.weight) {
-                gn_params<VEC>(a.weight, pofs + c, w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] *= w[e];
-            }
-            if (a.bias) {
-                gn_params<VEC>(a.bias, pofs + c, w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] += w[e];
-            }
-            if (a.mode & kGnSilu) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] = silu(o[e]);
-            }
-            if (zp && !(a.mode & kGnGateFirst)) {
-                zv[i].get(w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] *= silu(w[e]);
-            }
-            GnVec<T, VEC>::store(yp + c, o);
+        item += step;
+        row += row_step;
+        grp += grp_step;
+        if (grp >= a.groups) {
+            grp -= a.groups;
+            ++row;
         }
     }
 }

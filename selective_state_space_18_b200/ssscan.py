@@ -65,6 +65,8 @@ class SSError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Load (once) and return the ctypes handle of ``libssscan.so``."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -692,31 +694,36 @@ def _on_launch_stream(fn):
 
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
-        dev = (args[0] if args else kwargs[lead]).device
-        if dev.type != "cuda":
+        first = args[0] if args else kwargs[lead]
+        index = first.get_device()
+        if index < 0:
             raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
         if stream is None:
-            if torch.cuda.current_device() == dev.index:
+            if torch.cuda.current_device() == index:
                 return fn(*args, **kwargs)
-            with torch.cuda.device(dev):
+            with torch.cuda.device(index):
                 return fn(*args, **kwargs)
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        if stream.device != first.device:
+            raise ValueError(f"stream is on {stream.device}, expected {first.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)
     return wrapper
 
 
-def _rows_of(t, name, dev, dtype, shape):
-    """A tensor [..., heads, d] whose rows (all but the last two dimensions) the library
-    reads in place: (tensor, elements between rows).  A view that is not evenly strided
-    rows of packed heads is copied."""
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _check(t, name, index, dtype, shape):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows_of(t, name, index, dtype, shape):
+    """A tensor [..., heads, d] whose rows (all but the last two dimensions) the library
+    reads in place: (tensor, elements between rows).  A view that is not evenly strided
+    rows of packed heads is copied."""
+    _check(t, name, index, dtype, shape)
     width = shape[-2] * shape[-1]
     if t.is_contiguous():
         return t, width
@@ -733,12 +740,22 @@ def _rows_of(t, name, dev, dtype, shape):
     return t.contiguous(), width
 
 
-def _gate(t, name, dev, shape):
-    return None if t is None else _prep(t, name, dev, torch.float32, shape)
+def _dense(t, name, index, dtype, shape):
+    """An optional tensor as (tensor or None, address or None), copied when not contiguous."""
+    if t is None:
+        return None, None
+    _check(t, name, index, dtype, shape)
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t, t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _dense_out(t, name, index, dtype, shape):
+    """A caller-supplied output: written in place, so it must already be contiguous."""
+    _check(t, name, index, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
 
 
 def _delta_sizes(fn, q, v, lead):
@@ -749,6 +766,11 @@ def _delta_sizes(fn, q, v, lead):
     if hk == 0 or hv % hk:
         raise ValueError(f"{fn}: {hv} value heads are not a multiple of {hk} key heads")
     return hk, hv, dk, dv
+
+
+# the address of the current stream of a device, without building a Stream object
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @_on_launch_stream
@@ -765,43 +787,44 @@ def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None
 
     workspace: True (allocated for the call), False (none: the token-by-token kernel) or a
     uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself."""
-    dev, dt = q.device, q.dtype
+    index, dt = q.get_device(), q.dtype
     code = _dtype_code(q)
     hk, hv, dk, dv = _delta_sizes("ss_delta_scan", q, v, 2)
     bt, L = q.shape[:2]
-    q, qs = _rows_of(q, "q", dev, dt, (bt, L, hk, dk))
-    k, ks = _rows_of(k, "k", dev, dt, (bt, L, hk, dk))
-    v, vs = _rows_of(v, "v", dev, dt, (bt, L, hv, dv))
-    g = _gate(g, "g", dev, (bt, L, hv))
-    beta = _gate(beta, "beta", dev, (bt, L, hv))
-    h0 = _gate(h0, "h0", dev, (bt, hv, dk, dv))
+    q, qs = _rows_of(q, "q", index, dt, (bt, L, hk, dk))
+    k, ks = _rows_of(k, "k", index, dt, (bt, L, hk, dk))
+    v, vs = _rows_of(v, "v", index, dt, (bt, L, hv, dv))
+    g, pg = _dense(g, "g", index, torch.float32, (bt, L, hv))
+    beta, pb = _dense(beta, "beta", index, torch.float32, (bt, L, hv))
+    h0, ph = _dense(h0, "h0", index, torch.float32, (bt, hv, dk, dv))
+    pr = None
     if reset is not None:
-        reset = _prep(reset, "reset", dev, None, (bt, L))
-        if reset.dtype == torch.bool:
-            reset = reset.view(torch.uint8)
-        elif reset.dtype != torch.uint8:
+        if reset.dtype != torch.bool and reset.dtype != torch.uint8:
             raise TypeError("reset must be bool or uint8")
+        reset, pr = _dense(reset, "reset", index, reset.dtype, (bt, L))
     if outputs is None:
-        outputs = torch.empty((bt, L, hv, dv), device=dev, dtype=dt)
+        outputs = q.new_empty((bt, L, hv, dv))
     else:
-        outputs = _out(outputs, "outputs", dev, dt, (bt, L, hv, dv))
+        _dense_out(outputs, "outputs", index, dt, (bt, L, hv, dv))
     if final_state is not None:
-        final_state = _out(final_state, "final_state", dev, torch.float32, (bt, hv, dk, dv))
+        _dense_out(final_state, "final_state", index, torch.float32, (bt, hv, dk, dv))
     elif return_final_state:
-        final_state = torch.empty((bt, hv, dk, dv), device=dev, dtype=torch.float32)
+        final_state = q.new_empty((bt, hv, dk, dv), dtype=torch.float32)
     lib = load_library()
+    pw, nw = None, 0
     if workspace is True:
-        need = lib.ss_delta_workspace_bytes(bt, L, hk, hv, dk, dv, code)
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
-    elif workspace is False:
-        workspace = None
-    elif workspace is not None and (workspace.device != dev or workspace.dtype != torch.uint8
-                                    or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    st = lib.ss_delta_scan(bt, L, hk, hv, dk, dv, code, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(g),
-                           _addr(beta), _addr(reset), _addr(h0), dk ** -0.5 if scale is None else float(scale),
-                           SS_QK_L2NORM if qk_l2norm else 0, outputs.data_ptr(), _addr(final_state), _addr(workspace),
-                           0 if workspace is None else workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+        nw = lib.ss_delta_workspace_bytes(bt, L, hk, hv, dk, dv, code)
+        if nw:
+            workspace = q.new_empty(nw, dtype=torch.uint8)
+            pw = workspace.data_ptr()
+    elif workspace is not None and workspace is not False:
+        if workspace.get_device() != index or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+        pw, nw = workspace.data_ptr(), workspace.numel()
+    st = lib.ss_delta_scan(bt, L, hk, hv, dk, dv, code, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, pg, pb,
+                           pr, ph, dk ** -0.5 if scale is None else scale, SS_QK_L2NORM if qk_l2norm else 0,
+                           outputs.data_ptr(), None if final_state is None else final_state.data_ptr(), pw, nw,
+                           _raw_stream(index))
     if st != 0:
         raise SSError("ss_delta_scan", st)
     return {"outputs": outputs, "final_state": final_state}
@@ -818,26 +841,24 @@ def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=
     """Decode step of the gated delta rule: ``state`` [batch, heads_v, dk, dv] float32 is
     updated in place by one token.  q, k: [batch, heads_k, dk]; v: [batch, heads_v, dv];
     g, beta: [batch, heads_v] float32 or None.  Returns y [batch, heads_v, dv]."""
-    dev, dt = state.device, q.dtype
+    index, dt = state.get_device(), q.dtype
     code = _dtype_code(q)
     hk, hv, dk, dv = _delta_sizes("ss_delta_update", q, v, 1)
     bt = q.shape[0]
     if state.dtype != torch.float32 or state.shape != (bt, hv, dk, dv) or not state.is_contiguous():
         raise ValueError(f"state must be a contiguous float32 tensor of shape {(bt, hv, dk, dv)} (updated in place)")
-    q, qs = _rows_of(q, "q", dev, dt, (bt, hk, dk))
-    k, ks = _rows_of(k, "k", dev, dt, (bt, hk, dk))
-    v, vs = _rows_of(v, "v", dev, dt, (bt, hv, dv))
-    g = _gate(g, "g", dev, (bt, hv))
-    beta = _gate(beta, "beta", dev, (bt, hv))
+    q, qs = _rows_of(q, "q", index, dt, (bt, hk, dk))
+    k, ks = _rows_of(k, "k", index, dt, (bt, hk, dk))
+    v, vs = _rows_of(v, "v", index, dt, (bt, hv, dv))
+    g, pg = _dense(g, "g", index, torch.float32, (bt, hv))
+    beta, pb = _dense(beta, "beta", index, torch.float32, (bt, hv))
     if y is None:
-        y = torch.empty((bt, hv, dv), device=dev, dtype=dt)
+        y = q.new_empty((bt, hv, dv))
     else:
-        y = _out(y, "y", dev, dt, (bt, hv, dv))
+        _dense_out(y, "y", index, dt, (bt, hv, dv))
     st = load_library().ss_delta_update(bt, hk, hv, dk, dv, code, state.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
-                                        v.data_ptr(), vs, _addr(g), _addr(beta),
-                                        dk ** -0.5 if scale is None else float(scale),
-                                        SS_QK_L2NORM if qk_l2norm else 0, y.data_ptr(),
-                                        torch.cuda.current_stream(dev).cuda_stream)
+                                        v.data_ptr(), vs, pg, pb, dk ** -0.5 if scale is None else scale,
+                                        SS_QK_L2NORM if qk_l2norm else 0, y.data_ptr(), _raw_stream(index))
     if st != 0:
         raise SSError("ss_delta_update", st)
     return y
@@ -852,46 +873,49 @@ def ss_group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=Fa
     silu(gate); with ``gate_first`` the gate multiplies x before the statistics instead.
     x, gate, y: [..., channels] float32 or bfloat16; weight, bias: float32 [channels], or
     [channels // groups] for one set shared by all groups (both alike)."""
-    dev, dt = x.device, x.dtype
+    index, dt = x.get_device(), x.dtype
     code = _dtype_code(x)
     if x.dim() < 1:
         raise ValueError("x must have a channel dimension")
-    shape, ch = x.shape, x.shape[-1]
-    groups = int(groups)
+    shape = x.shape
+    ch = shape[-1]
     if groups <= 0 or ch % groups:
         raise ValueError(f"{ch} channels do not divide into {groups} groups")
     size = ch // groups
-    if activation not in (None, "silu"):
+    if activation is not None and activation != "silu":
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-
-    def rows(t, name):
-        if t.device != dev or t.dtype != dt or t.shape != shape:
-            raise ValueError(f"{name} must be a {dt} tensor of shape {tuple(shape)} on {dev}")
-        t = t.reshape(-1, ch)
-        if t.shape[0] <= 1:
-            return t.contiguous(), ch
-        if (t.stride(1) != 1 and ch > 1) or t.stride(0) < ch:
-            t = t.contiguous()
-        return t, t.stride(0)
-
-    params = [t for t in (weight, bias) if t is not None]
-    shared = bool(params) and params[0].shape == (size,) and groups > 1
-    for t in params:
-        if t.device != dev or t.dtype != torch.float32 or t.shape != ((size,) if shared else (ch,)):
-            raise ValueError(f"weight and bias must be float32 tensors of shape ({ch},) or both ({size},) on {dev}")
-    weight = None if weight is None else weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    x, xs = rows(x, "x")
-    gate, zs = rows(gate, "gate") if gate is not None else (None, 0)
-    if y is None:
-        y = torch.empty(shape, device=dev, dtype=dt)
-    else:
-        y = _out(y, "y", dev, dt, shape)
+    x, xs = _channel_rows(x, ch)
+    pz, zs = None, 0
+    if gate is not None:
+        _check(gate, "gate", index, dt, shape)
+        gate, zs = _channel_rows(gate, ch)
+        pz = gate.data_ptr()
     flags = ((SS_NORM_CENTER if center else 0) | (SS_NORM_GATE_FIRST if gate_first else 0)
-             | (SS_NORM_SILU if activation else 0) | (SS_NORM_SHARED if shared else 0))
-    st = load_library().ss_group_norm(x.shape[0], groups, size, code, x.data_ptr(), xs, _addr(gate), zs, _addr(weight),
-                                      _addr(bias), float(eps), flags, y.data_ptr(),
-                                      torch.cuda.current_stream(dev).cuda_stream)
+             | (SS_NORM_SILU if activation else 0))
+    width = (ch,)
+    first = weight if weight is not None else bias
+    if first is not None and groups > 1 and first.shape == (size,):
+        width = (size,)
+        flags |= SS_NORM_SHARED
+    weight, pwt = _dense(weight, "weight", index, torch.float32, width)
+    bias, pbs = _dense(bias, "bias", index, torch.float32, width)
+    if y is None:
+        y = x.new_empty(shape)
+    else:
+        _dense_out(y, "y", index, dt, shape)
+    st = load_library().ss_group_norm(x.shape[0], groups, size, code, x.data_ptr(), xs, pz, zs, pwt, pbs, eps, flags,
+                                      y.data_ptr(), _raw_stream(index))
     if st != 0:
         raise SSError("ss_group_norm", st)
     return y
+
+
+def _channel_rows(t, ch):
+    """[..., channels] as rows: (2-D tensor, elements between rows); a view whose rows are
+    not evenly strided runs of channels is copied."""
+    if t.dim() != 2:
+        t = t.reshape(-1, ch)
+    rows, step = t.shape[0], t.stride(0)
+    if (t.stride(1) == 1 or ch == 1) and (step >= ch or rows <= 1):
+        return t, step if rows > 1 else ch
+    return t.contiguous(), ch

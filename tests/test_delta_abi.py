@@ -120,15 +120,14 @@ def test_binding_refuses():
 
 def test_row_views_are_recognised():
     """Slices of one projection are read in place; other views are copied."""
-    dev = torch.device("cpu")
     qkv = torch.arange(2 * 3 * 40.0).view(2, 3, 40)
     k = qkv[..., 8:24].unflatten(-1, (2, 8))
-    t, step = ssscan._rows_of(k, "k", dev, torch.float32, (2, 3, 2, 8))
+    t, step = ssscan._rows_of(k, "k", -1, torch.float32, (2, 3, 2, 8))
     assert step == 40 and t.data_ptr() == k.data_ptr()
-    assert ssscan._rows_of(k[:, :1], "k", dev, torch.float32, (2, 1, 2, 8))[1] == 120
-    assert ssscan._rows_of(k[1:, :1], "k", dev, torch.float32, (1, 1, 2, 8))[1] == 16
+    assert ssscan._rows_of(k[:, :1], "k", -1, torch.float32, (2, 1, 2, 8))[1] == 120
+    assert ssscan._rows_of(k[1:, :1], "k", -1, torch.float32, (1, 1, 2, 8))[1] == 16
     for bad in (k[:, ::2], k.transpose(0, 1), k[..., ::2], k[:, :, ::2], k[:1].expand(2, -1, -1, -1)):
-        t, step = ssscan._rows_of(bad, "k", dev, torch.float32, bad.shape)
+        t, step = ssscan._rows_of(bad, "k", -1, torch.float32, bad.shape)
         assert torch.equal(t, bad)
         rows = t.as_strided((bad.shape[0] * bad.shape[1], bad.shape[2] * bad.shape[3]), (step, 1), t.storage_offset())
         assert torch.equal(rows, bad.reshape(rows.shape))
