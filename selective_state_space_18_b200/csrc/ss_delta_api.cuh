@@ -78,6 +78,21 @@ bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
            batch < (int64_t(1) << 31);
 }
 
+// Segments of the two-pass walk (1: one pass).  A walk is one of two on its SM; with S
+// segments pass 1 needs a walk per head and column tile for each of S - 1 segments and one
+// more (for M) in S - 2 of them, and all of those should run at once: that bounds S.  Two
+// passes over 1/S of the chunks, each step up to 1.3 times as long with two walks on an SM,
+// and the join pay from S = 3 on and for segments of at least four chunks.
+constexpr int64_t kDeltaWalkSlots = 2 * 148;
+int64_t delta_segments(int64_t heads, int64_t tiles, int64_t chunks)
+{
+    // heads * (tiles + (S - 2) * (tiles + 1)) <= slots
+    const int64_t room = kDeltaWalkSlots / heads - tiles;
+    int64_t segs = room < 0 ? 1 : 2 + room / (tiles + 1);
+    segs = segs < chunks / 4 ? segs : chunks / 4;
+    return segs < 3 ? 1 : segs;
+}
+
 bool delta_chunked(const ss::DeltaArgs &a, const void *workspace)
 {
     return workspace && delta_chunked_shape(a.batch, a.seq, a.dk, a.dv, SS_BF16) && aligned(a.q, 16) &&
@@ -104,8 +119,8 @@ bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, 
 }
 
 template <int MT>
-int launch_delta_walk(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps, unsigned grid, uint32_t *status,
-                      cudaStream_t s)
+int launch_delta_walk_t(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps, unsigned grid, uint32_t *status,
+                        cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
     const int st = ensure_smem(ss::ss_delta_walk_kernel<MT>, size_t(ss::DwSmem::kBytes), smem_done);
@@ -115,6 +130,19 @@ int launch_delta_walk(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps,
     return launch_status();
 }
 
+// Up to one walk per SM: sixteen compute warps each; more: two CTAs of eight per SM.
+int launch_delta_walk(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps, int64_t grid, uint32_t *status,
+                      cudaStream_t s)
+{
+    int sms = 0;
+    if (device_sm_count(&sms) != SS_OK)
+        return SS_ERR_CUDA;
+    if (grid > 0x7fffffffLL)
+        return SS_ERR_SHAPE;
+    return grid <= sms ? launch_delta_walk_t<1>(w, maps, unsigned(grid), status, s)
+                       : launch_delta_walk_t<2>(w, maps, unsigned(grid), status, s);
+}
+
 int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
@@ -122,8 +150,7 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     if (st != SS_OK)
         return st;
     uint32_t *status = nullptr;
-    int sms = 0;
-    if (status_word_address(&status) != SS_OK || device_sm_count(&sms) != SS_OK)
+    if (status_word_address(&status) != SS_OK)
         return SS_ERR_CUDA;
     ss::DeltaPrepArgs p{};
     p.d = a;
@@ -140,6 +167,11 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     w.col_tiles = (a.dv + 127) / 128;
     w.nks = (a.dk + 15) / 16;
     w.blocks = p.blocks;
+    const int64_t segs = delta_segments(a.batch * a.heads_v, w.col_tiles, p.nchunks);
+    w.seg_chunks = int((p.nchunks + segs - 1) / segs);
+    w.segments = (p.nchunks + w.seg_chunks - 1) / w.seg_chunks;
+    w.seg_n = reinterpret_cast<float *>(p.blocks + a.batch * a.heads_v * p.nchunks * ss::kDcBlockBytes);
+    w.seg_m = w.seg_n + a.batch * a.heads_v * (w.segments - 1) * a.dk * a.dv;
     w.h0 = a.h0;
     w.g = a.g;
     w.reset = a.reset;
@@ -158,9 +190,18 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     ss::ss_delta_prep_kernel<<<unsigned(units), ss::kDpThreads, ss::DeltaPrepSmem::kBytes, s>>>(p);
     if ((st = launch_status()) != SS_OK)
         return st;
-    // up to one walk per SM: sixteen compute warps each; more: two CTAs of eight per SM
-    return grid <= sms ? launch_delta_walk<1>(w, maps, unsigned(grid), status, s)
-                       : launch_delta_walk<2>(w, maps, unsigned(grid), status, s);
+    if (w.segments == 1)
+        return launch_delta_walk(w, maps, grid, status, s);
+    const int64_t heads = a.batch * a.heads_v;
+    w.pass = 1;
+    st = launch_delta_walk(w, maps, heads * (w.col_tiles + (w.segments - 2) * (w.col_tiles + 1)), status, s);
+    if (st != SS_OK)
+        return st;
+    ss::ss_delta_join_kernel<<<unsigned(heads * ((a.dv + ss::kDjCols - 1) / ss::kDjCols)), ss::kDjThreads, 0, s>>>(w);
+    if ((st = launch_status()) != SS_OK)
+        return st;
+    w.pass = 2;
+    return launch_delta_walk(w, maps, heads * w.col_tiles * w.segments, status, s);
 }
 
 template <typename T, int J> int launch_delta_update(ss::DeltaUpdateArgs a, cudaStream_t s)
@@ -300,11 +341,13 @@ int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, in
     if (batch <= 0 || seq <= 0 || heads_k <= 0 || heads_v <= 0 || dk <= 0 || dv <= 0 || heads_v % heads_k ||
         !delta_chunked_shape(batch, seq, dk, dv, dtype))
         return 0;
-    int64_t n = 0;
+    int64_t heads = 0, n = 0;
     const int64_t chunks = (seq + ss::kDcChunk - 1) / ss::kDcChunk;
-    if (!mul_ok(batch, heads_v, &n) || !mul_ok(n, chunks, &n) || !mul_ok(n, ss::kDcBlockBytes, &n))
+    if (!mul_ok(batch, heads_v, &heads) || !mul_ok(heads, chunks, &n) || !mul_ok(n, ss::kDcBlockBytes, &n))
         return 0;
-    return n;
+    // the states of the segments, when the sequence is cut (few heads: they are small)
+    const int64_t segs = delta_segments(heads, (dv + 127) / 128, chunks);
+    return segs == 1 ? n : n + heads * 4 * dk * ((segs - 1) * dv + (segs - 2) * dk);
 }
 
 int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,

@@ -31,6 +31,15 @@
 // beyond 2^-60 in all, the walk scales the rows of Q by s in shared memory instead and
 // takes P itself (the block says which).
 //
+// Few heads and a long prompt leave most SMs without a walk.  The sequence is then cut into
+// segments that are walked at once, in two passes ("s6_reset" blog draft, Associative
+// Boundary Resetting, for matrix states): a segment acts on the state that enters it as
+// S -> M S + N, so pass 1 walks every segment but the last for N, its end state from zero
+// (the first from h0), and every one but the first and the last for M, its end state from
+// the identity with v = 0; ss_delta_join_kernel chains them in fp32, and pass 2 walks every
+// segment from its entering state with outputs.  That is the work of three walks in the
+// time of two segments.
+//
 // Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
 // state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
 // products summed in fp32, so the final state follows fp32 arithmetic to about 5e-6 of
@@ -44,7 +53,7 @@
 // zero in fp32 (a reset, -inf, below 2^-160) cuts: cut counts tell which pairs it parts.
 // A cut at a chunk's first token leaves the chunk itself alone: the chunk before it hands
 // on a state of zero (and h0 is not read).  A sequence without h0 begins the same way, so
-// a document that starts a chunk gives the same bits as on its own.
+// within a segment a document that starts a chunk gives the same bits as on its own.
 #pragma once
 
 #include <cuda.h>
@@ -508,6 +517,10 @@ struct DeltaWalkArgs {
     int64_t batch;
     int seq, heads_v, ratio, dk, dv;
     int nchunks, col_tiles, nks;  // nks: 16-key slices of the state
+    int segments, seg_chunks;     // 1 segment: one pass over all chunks
+    int pass;                     // 0, or 1 and 2 (see above)
+    float *seg_n;                 // [batch, heads_v, segments - 1, dk, dv]: N, then the state after the segment
+    float *seg_m;                 // [batch, heads_v, segments - 2, dk, dk]: M of segments 1 ..
     const unsigned char *blocks;
     const float *h0;              // nullable
     const float *g;               // nullable; g and reset for the first token
@@ -619,11 +632,30 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const bool issuer = warp == kWarps;
-    const int tile = int(blockIdx.x % unsigned(a.col_tiles));
-    const int64_t bh = blockIdx.x / unsigned(a.col_tiles);
+    // (head, segment, column tile); tile col_tiles of pass 1 is the walk for M
+    int tile, seg = 0;
+    int64_t bh;
+    if (a.pass == 1) {
+        const unsigned per = unsigned(a.col_tiles + (a.segments - 2) * (a.col_tiles + 1));
+        bh = blockIdx.x / per;
+        tile = int(blockIdx.x % per);
+        if (tile >= a.col_tiles) {
+            seg = 1 + (tile - a.col_tiles) / (a.col_tiles + 1);
+            tile = (tile - a.col_tiles) % (a.col_tiles + 1);
+        }
+    } else {
+        const unsigned per = unsigned(a.segments * a.col_tiles);
+        bh = blockIdx.x / per;
+        seg = int(blockIdx.x % per) / a.col_tiles;
+        tile = int(blockIdx.x % per) % a.col_tiles;
+    }
+    const bool outs = a.pass != 1, for_m = tile == a.col_tiles;
     const int64_t b = bh / a.heads_v;
     const int h = int(bh % a.heads_v), hk = h / a.ratio;
-    const int n0 = 128 * tile;
+    const int n0 = for_m ? 0 : 128 * tile;
+    const int cols = for_m ? a.dk : a.dv; // columns of the state walked
+    const int cb = seg * a.seg_chunks;    // the segment's chunks: cb + c, c < nc
+    const int nc = a.nchunks - cb < a.seg_chunks ? a.nchunks - cb : a.seg_chunks;
     const uint32_t s_base = smem_u32(sm);
 
     if (tid == 0) {
@@ -650,7 +682,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         // ======================= the issuer warp (one thread works) =======================
         if (elect_one()) {
             const int32_t b32 = int32_t(b);
-            const unsigned char *blocks = a.blocks + bh * a.nchunks * kDcBlockBytes;
+            const unsigned char *blocks = a.blocks + (bh * a.nchunks + cb) * kDcBlockBytes;
+            const int t_first = cb * kDcChunk;
             // barriers with a phase begun by a load or a product, and its parity
             uint32_t begun = 0, latest = ~0u;
             auto begin = [&](const uint64_t *bar) {
@@ -662,7 +695,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 begin(bar);
             };
             auto load_kb = [&](int c) {
-                const int st = c & 1, t = c * kDcChunk;
+                const int st = c & 1, t = t_first + c * kDcChunk;
                 begin(bar_k + st);
                 begin(bar_b + st);
                 mbar_arrive_expect_tx(bar_k + st, 16384);
@@ -679,26 +712,29 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             auto load_q = [&](int c) {
                 begin(bar_q);
                 mbar_arrive_expect_tx(bar_q, 16384);
-                tma_load_4d(sm + DwSmem::kQ, &maps.q, 0, hk, c * kDcChunk, b32, bar_q);
-                tma_load_4d(sm + DwSmem::kQ + 8192, &maps.q, 64, hk, c * kDcChunk, b32, bar_q);
+                tma_load_4d(sm + DwSmem::kQ, &maps.q, 0, hk, t_first + c * kDcChunk, b32, bar_q);
+                tma_load_4d(sm + DwSmem::kQ + 8192, &maps.q, 64, hk, t_first + c * kDcChunk, b32, bar_q);
             };
             auto load_v = [&](int c) {
                 begin(bar_v);
                 mbar_arrive_expect_tx(bar_v, 16384);
-                tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, c * kDcChunk, b32, bar_v);
-                tma_load_4d(sm + DwSmem::kV + 8192, &maps.v, n0 + 64, h, c * kDcChunk, b32, bar_v);
+                tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, t_first + c * kDcChunk, b32, bar_v);
+                tma_load_4d(sm + DwSmem::kV + 8192, &maps.v, n0 + 64, h, t_first + c * kDcChunk, b32, bar_v);
             };
             constexpr uint32_t kIdTok = idesc_bf16(128, kDcChunk, 0, 0), kIdHalf = idesc_bf16(128, 32, 0, 0);
             // dH in halves of 64 keys
             const int nk0 = a.nks < 4 ? a.nks : 4;
             const uint32_t id_dh0 = idesc_bf16(128, 16 * nk0, 0, 1), id_dh1 = idesc_bf16(128, 16 * (a.nks - nk0), 0, 1);
             load_kb(0);
-            load_q(0);
-            load_v(0);
-            load_p(0);
-            if (a.nchunks > 1)
+            if (!for_m)
+                load_v(0);
+            if (outs) {
+                load_q(0);
+                load_p(0);
+            }
+            if (nc > 1)
                 load_kb(1);
-            for (int c = 0; c < a.nchunks; ++c) {
+            for (int c = 0; c < nc; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
                 const uint32_t kb = s_base + DwSmem::kK + st * 16384, bb = s_base + DwSmem::kB + st * kDcHead;
@@ -717,8 +753,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 // the products of c - 1, the last readers of the other stage and of P, completed
                 // before H(c) was written
                 if (c > 0) {
-                    load_p(c);
-                    if (c + 1 < a.nchunks)
+                    if (outs)
+                        load_p(c);
+                    if (c + 1 < nc)
                         load_kb(c + 1);
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
@@ -740,38 +777,48 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                 }
                 commit(bar_u);
-                if (c + 1 < a.nchunks) // R(c), the only reader of v, is written
+                if (c + 1 < nc && !for_m) // R(c), the only reader of v, is written
                     load_v(c + 1);
-                // Y^T over R: H^T Q^T, once R has been read
-                if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status) || !mbar_wait(bar_u, ph, status)) {
-                    ok = false;
-                    break;
+                if (outs) {
+                    // Y^T over R: H^T Q^T, once R has been read
+                    if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status) ||
+                        !mbar_wait(bar_u, ph, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int ks = 0; ks < a.nks; ++ks) {
+                        const uint32_t qo = s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32;
+                        umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
+                        umma_bf16_ts(tmem + kDwD1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf,
+                                     ks > 0);
+                    }
+                    commit(bar_qh);
                 }
-                tc_fence_after();
-                for (int ks = 0; ks < a.nks; ++ks) {
-                    const uint32_t qo = s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32;
-                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
-                    umma_bf16_ts(tmem + kDwD1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf,
-                                 ks > 0);
-                }
-                commit(bar_qh);
                 // + U^T P^T, and dH^T over H, once U is written and H has been read: its first
                 // half while U^T P^T completes, whose U lies in the place of the second
-                if (!mbar_wait(bar_p, ph, status) || !mbar_wait(arr_u, ph, status)) {
+                if (!mbar_wait(arr_u, ph, status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if (outs) {
+                    if (!mbar_wait(bar_p, ph, status)) {
+                        ok = false;
+                        break;
+                    }
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
+                    for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                    for (int ks = 0; ks < 2 + 2 * hf; ++ks)
-                        umma_bf16_ts(tmem + kDwD1 + 32 * hf, tmem + kDwU + 16 * ks,
-                                     sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
-                commit(bar_y);
-                if (!mbar_wait(bar_qh, ph, status)) {
-                    ok = false;
-                    break;
+                        for (int ks = 0; ks < 2 + 2 * hf; ++ks)
+                            umma_bf16_ts(tmem + kDwD1 + 32 * hf, tmem + kDwU + 16 * ks,
+                                         sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)),
+                                         kIdHalf, 1);
+                    commit(bar_y);
+                    if (!mbar_wait(bar_qh, ph, status)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_after();
 #pragma unroll
@@ -782,7 +829,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
                 commit(bar_dh);
                 if (a.nks > 4) {
-                    if (!mbar_wait(bar_y, ph, status)) {
+                    if (outs && !mbar_wait(bar_y, ph, status)) {
                         ok = false;
                         break;
                     }
@@ -795,7 +842,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                 }
                 commit(bar_dh + 1);
-                if (c + 1 < a.nchunks)
+                if (c + 1 < nc && outs)
                     load_q(c + 1);
             }
             // let every load and product in flight finish before the tensor memory is freed:
@@ -816,17 +863,26 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         const uint32_t lanes = tmem + (uint32_t(row0) << 16);
         // H[m][k][x]: value column col + 16 m + 8 x, keys 64 cg + 8 k + tc, + 1
         float2 H[MT][8][2];
-        const int64_t sofs = (bh * a.dk + 64 * cg + tc) * a.dv + col;
-        const bool enter = a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h);
+        // the state the segment starts from: h0, the state after the segment before it, the
+        // identity, or zero
+        const float *from = nullptr;
+        if (a.pass == 2 && seg > 0)
+            from = a.seg_n + (bh * (a.segments - 1) + seg - 1) * a.dk * a.dv;
+        else if (seg == 0 && a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h))
+            from = a.h0 + bh * a.dk * a.dv;
+        const int64_t sofs = int64_t(64 * cg + tc) * cols + col;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const bool in = enter && 64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < a.dv; // (dk is even)
-                    const int64_t o = sofs + int64_t(8 * k) * a.dv + 16 * m + 8 * x;
-                    H[m][k][x] = make_float2(in ? a.h0[o] : 0.0f, in ? a.h0[o + a.dv] : 0.0f);
+                    const int key = 64 * cg + 8 * k + tc, vc = col + 16 * m + 8 * x;
+                    const bool in = from && key < a.dk && vc < cols; // (dk is even)
+                    const int64_t o = sofs + int64_t(8 * k) * cols + 16 * m + 8 * x;
+                    H[m][k][x] = make_float2(in ? from[o] : 0.0f, in ? from[o + cols] : 0.0f);
+                    if (for_m) // the identity
+                        H[m][k][x] = make_float2(key == vc ? 1.0f : 0.0f, key + 1 == vc ? 1.0f : 0.0f);
                 }
         // 16 keys (2 k-blocks from kb) of tile m as operand columns
         auto store_h = [&](int m, int kb) {
@@ -861,9 +917,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         const uint32_t y_base = smem_u32(ytile);
         // this lane's 16 bytes of the tile's first rows; rows 32 >> MT further on, ystep more
         const int64_t ystep = int64_t(32 >> MT) * a.heads_v * a.dv;
-        __nv_bfloat16 *yp = a.y + ((b * a.seq + 32 * cg + (lane >> MT)) * a.heads_v + h) * a.dv + n0 + row0 +
+        __nv_bfloat16 *yp = a.y + ((b * a.seq + cb * kDcChunk + 32 * cg + (lane >> MT)) * a.heads_v + h) * a.dv + n0 + row0 +
                             8 * (lane & (2 * MT - 1));
-        for (int c = 0; c < a.nchunks; ++c) {
+        for (int c = 0; c < nc; ++c) {
             const int st = c & 1;
             const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
             const unsigned char *blk = sm + DwSmem::kB + st * kDcHead;
@@ -880,7 +936,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             }
             const float2 em = *reinterpret_cast<const float2 *>(blk + kDcE); // E_63, mode
             // ---- s o Q in place (bf16), in chunks whose decays leave the range of P' ---------
-            if (em.y != 0.0f) {
+            if (outs && em.y != 0.0f) {
                 if (!wait(bar_q, ph)) {
                     ok = false;
                     break;
@@ -902,19 +958,21 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             }
             arrive(arr_q);
             // ---- R^T = V^T - KH^T diag(c) -------------------------------------------------
-            if (!wait(bar_v, ph) || !wait(bar_kh, ph)) {
+            if ((!for_m && !wait(bar_v, ph)) || !wait(bar_kh, ph)) {
                 ok = false;
                 break;
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg;
-                uint32_t r[16], v[2][4];
+                uint32_t r[16], v[2][4] = {};
                 // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
+                if (!for_m) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
+                    for (int j = 0; j < 2; ++j)
+                        ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
                                                                ((row0 & 63) >> 3) + 2 * m + ((ln >> 3) & 1)));
+                }
                 tmem_ld_frag(at, r);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -967,49 +1025,51 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             tmem_st_wait();
             arrive(arr_u);
             // ---- while dH^T runs: the outputs ---------------------------------------------
-            if (!wait(bar_y, ph)) {
-                ok = false;
-                break;
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                uint32_t r[16];
-                tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg, r);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = 2 * j + i;
-                        float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
-                        sv.x = em.y == 0.0f ? sv.x : 1.0f;
-                        sv.y = em.y == 0.0f ? sv.y : 1.0f;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * k + x));
-                            o[2 * i + x] = pack_bf16x2(y.x, y.y);
-                        }
-                    }
-                    // rows of 32 MT bytes (16 MT values) in the swizzle of that span: token 8 (2 j +
-                    // matrix / 2) + lane % 8, values 16 m + 8 (matrix % 2) ..
-                    const int t = 16 * j + 8 * (ln >> 4) + (ln & 7), ch = 2 * m + ((ln >> 3) & 1);
-                    stmatrix_x4_trans(y_base + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1)), o);
+            if (outs) {
+                if (!wait(bar_y, ph)) {
+                    ok = false;
+                    break;
                 }
-            }
-            __syncwarp();
-            // back as rows of the tile, 16 bytes a lane (a TMA store per warp and the proxy fence
-            // before it took three times as long)
-            {
-                const int t = ln >> MT, ch = ln & (2 * MT - 1); // (the swizzle repeats every 8 rows)
-                const unsigned char *src = ytile + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1));
-                const int left = a.seq - c * kDcChunk - 32 * cg - t;
-                const bool in = n0 + row0 + 8 * ch < a.dv; // (dv is a multiple of 8)
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-                    if (in && left > (32 >> MT) * i)
-                        *reinterpret_cast<uint4 *>(yp + i * ystep) =
-                            *reinterpret_cast<const uint4 *>(src + 32 * MT * (32 >> MT) * i);
-                yp += (2 << MT) * ystep;
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t r[16];
+                    tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg, r);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int k = 2 * j + i;
+                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
+                            sv.x = em.y == 0.0f ? sv.x : 1.0f;
+                            sv.y = em.y == 0.0f ? sv.y : 1.0f;
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * k + x));
+                                o[2 * i + x] = pack_bf16x2(y.x, y.y);
+                            }
+                        }
+                        // rows of 32 MT bytes (16 MT values) in the swizzle of that span: token 8 (2 j +
+                        // matrix / 2) + lane % 8, values 16 m + 8 (matrix % 2) ..
+                        const int t = 16 * j + 8 * (ln >> 4) + (ln & 7), ch = 2 * m + ((ln >> 3) & 1);
+                        stmatrix_x4_trans(y_base + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1)), o);
+                    }
+                }
+                __syncwarp();
+                // back as rows of the tile, 16 bytes a lane (a TMA store per warp and the proxy fence
+                // before it took three times as long)
+                {
+                    const int t = ln >> MT, ch = ln & (2 * MT - 1); // (the swizzle repeats every 8 rows)
+                    const unsigned char *src = ytile + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1));
+                    const int left = a.seq - (cb + c) * kDcChunk - 32 * cg - t;
+                    const bool in = n0 + row0 + 8 * ch < a.dv; // (dv is a multiple of 8)
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i)
+                        if (in && left > (32 >> MT) * i)
+                            *reinterpret_cast<uint4 *>(yp + i * ystep) =
+                                *reinterpret_cast<const uint4 *>(src + 32 * MT * (32 >> MT) * i);
+                    yp += (2 << MT) * ystep;
+                }
             }
             // ---- H = E_63 H + dH -------------------------------------------------------------
             if (!wait(bar_dh + cg, ph)) {
@@ -1037,17 +1097,25 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             tmem_st_wait();
             arrive(arr_h);
         }
-        if (ok && a.final_state) {
+        // where the state goes: N or M, or the final state after the last segment
+        float *to = nullptr;
+        if (for_m)
+            to = a.seg_m + (bh * (a.segments - 2) + seg - 1) * a.dk * a.dk;
+        else if (a.pass == 1)
+            to = a.seg_n + (bh * (a.segments - 1) + seg) * a.dk * a.dv;
+        else if (seg == a.segments - 1 && a.final_state)
+            to = a.final_state + bh * a.dk * a.dv;
+        if (ok && to) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < a.dv) {
-                            const int64_t o = sofs + int64_t(8 * k) * a.dv + 16 * m + 8 * x;
-                            a.final_state[o] = H[m][k][x].x;
-                            a.final_state[o + a.dv] = H[m][k][x].y;
+                        if (64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < cols) {
+                            const int64_t o = sofs + int64_t(8 * k) * cols + 16 * m + 8 * x;
+                            to[o] = H[m][k][x].x;
+                            to[o + cols] = H[m][k][x].y;
                         }
                     }
         }
@@ -1057,6 +1125,66 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     tc_fence_after();
     if (warp == 0)
         tmem_dealloc(tmem, kDwTmemCols);
+}
+
+// ---- the join ------------------------------------------------------------------------
+//
+// seg_n[s] <- M_s seg_n[s - 1] + seg_n[s] for s = 1 .. segments - 2, in order: the states
+// after the segments.  One CTA per head and 16 columns, the running state's columns in
+// shared memory, a row and 8 columns a thread; all fp32.  A few microseconds of latency.
+
+constexpr int kDjThreads = 256, kDjCols = 16;
+
+__global__ void __launch_bounds__(kDjThreads) ss_delta_join_kernel(const DeltaWalkArgs a)
+{
+    __shared__ __align__(16) float st[128][kDjCols];
+    const int tiles = (a.dv + kDjCols - 1) / kDjCols;
+    const int64_t bh = blockIdx.x / unsigned(tiles);
+    const int c0 = int(blockIdx.x % unsigned(tiles)) * kDjCols;
+    const int row = threadIdx.x >> 1, c = 8 * (threadIdx.x & 1);
+    const bool in = row < a.dk && c0 + c < a.dv; // (dv is a multiple of 8)
+    float *n = a.seg_n + bh * (a.segments - 1) * a.dk * a.dv + int64_t(row) * a.dv + c0 + c;
+    const float *m = a.seg_m + bh * (a.segments - 2) * a.dk * a.dk + int64_t(row) * a.dk;
+    const int64_t nstep = int64_t(a.dk) * a.dv, mstep = int64_t(a.dk) * a.dk;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        st[row][c + e] = in ? n[e] : 0.0f;
+    __syncthreads();
+    for (int s = 1; s < a.segments - 1; ++s) {
+        n += nstep;
+        float2 acc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] = in ? make_float2(n[2 * e], n[2 * e + 1]) : make_float2(0.0f, 0.0f);
+        if (in) {
+#pragma unroll 2
+            for (int k = 0; k < a.dk; k += 8) { // (dk is a multiple of 8)
+                float f[8];
+                *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(m + k);
+                *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(m + k + 4);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float4 lo = *reinterpret_cast<const float4 *>(&st[k + u][c]);
+                    const float4 hi = *reinterpret_cast<const float4 *>(&st[k + u][c + 4]);
+                    const float2 x = make_float2(f[u], f[u]);
+                    acc[0] = __ffma2_rn(x, make_float2(lo.x, lo.y), acc[0]);
+                    acc[1] = __ffma2_rn(x, make_float2(lo.z, lo.w), acc[1]);
+                    acc[2] = __ffma2_rn(x, make_float2(hi.x, hi.y), acc[2]);
+                    acc[3] = __ffma2_rn(x, make_float2(hi.z, hi.w), acc[3]);
+                }
+            }
+        }
+        __syncthreads();
+        if (in) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                st[row][c + 2 * e] = n[2 * e] = acc[e].x;
+                st[row][c + 2 * e + 1] = n[2 * e + 1] = acc[e].y;
+            }
+        }
+        __syncthreads();
+        m += mstep;
+    }
 }
 
 } // namespace ss

@@ -70,6 +70,18 @@ def test_long_ragged(orc, dtype):
     _check(orc, make_delta_inputs(1, 2051, 1, 2, 128, 128, dtype, seed=3100, h0=True), "long")
 
 
+@pytest.mark.parametrize("shape", [(1, 1300, 1, 1, 128, 128), (1, 1024, 2, 4, 64, 256), (2, 2000, 1, 3, 40, 24),
+                                   (1, 833, 4, 32, 128, 128), (3, 1531, 4, 12, 96, 64)])
+@pytest.mark.parametrize("resets", [0, 150])
+def test_segments(orc, shape, resets):
+    """Few heads and a long prompt: the sequence is cut and walked in two passes.  With
+    decays near one the segments' entering states matter over the whole sequence."""
+    inp = make_delta_inputs(*shape, "bf16", seed=3170 + sum(shape), h0=True, reset_mean_doc=resets or None)
+    _check(orc, inp, f"{shape}")
+    inp["g"] = inp["g"] * 1e-3
+    _check(orc, inp, f"{shape}, slow decay")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("workspace", [True, False])
 def test_without_norm_or_gates(orc, dtype, workspace):
