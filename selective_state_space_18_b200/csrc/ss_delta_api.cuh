@@ -78,17 +78,14 @@ bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
            batch < (int64_t(1) << 31);
 }
 
-// Segments of the two-pass walk (1: one pass).  A walk is one of two on its SM; with S
-// segments pass 1 needs a walk per head and column tile for each of S - 1 segments and one
-// more (for M) in S - 2 of them, and all of those should run at once: that bounds S.  Two
-// passes over 1/S of the chunks, each step up to 1.3 times as long with two walks on an SM,
-// and the join pay from S = 3 on and for segments of at least four chunks.
+// Segments of the two-pass walk (1: one pass): as many as make pass 2 fill the GPU with
+// two walks on every SM, three at least and four chunks each at least.  A step of a walk
+// takes 1.4 times as long beside another one, so S segments turn n steps into about
+// (1.4 + 1.2) n / S, or (1.4 + 2.4) n / S where every M has to be walked to the end.
 constexpr int64_t kDeltaWalkSlots = 2 * 148;
 int64_t delta_segments(int64_t heads, int64_t tiles, int64_t chunks)
 {
-    // heads * (tiles + (S - 2) * (tiles + 1)) <= slots
-    const int64_t room = kDeltaWalkSlots / heads - tiles;
-    int64_t segs = room < 0 ? 1 : 2 + room / (tiles + 1);
+    int64_t segs = heads > kDeltaWalkSlots ? 1 : kDeltaWalkSlots / (heads * tiles);
     segs = segs < chunks / 4 ? segs : chunks / 4;
     return segs < 3 ? 1 : segs;
 }
@@ -172,6 +169,7 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     w.segments = (p.nchunks + w.seg_chunks - 1) / w.seg_chunks;
     w.seg_n = reinterpret_cast<float *>(p.blocks + a.batch * a.heads_v * p.nchunks * ss::kDcBlockBytes);
     w.seg_m = w.seg_n + a.batch * a.heads_v * (w.segments - 1) * a.dk * a.dv;
+    w.seg_zero = reinterpret_cast<int *>(w.seg_m + a.batch * a.heads_v * (w.segments - 2) * a.dk * a.dk);
     w.h0 = a.h0;
     w.g = a.g;
     w.reset = a.reset;
@@ -197,7 +195,11 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     st = launch_delta_walk(w, maps, heads * (w.col_tiles + (w.segments - 2) * (w.col_tiles + 1)), status, s);
     if (st != SS_OK)
         return st;
-    ss::ss_delta_join_kernel<<<unsigned(heads * ((a.dv + ss::kDjCols - 1) / ss::kDjCols)), ss::kDjThreads, 0, s>>>(w);
+    static std::atomic<uint64_t> join_done{0};
+    if ((st = ensure_smem(ss::ss_delta_join_kernel, size_t(ss::kDjSmem), join_done)) != SS_OK)
+        return st;
+    ss::ss_delta_join_kernel<<<unsigned(heads * ((a.dv + ss::kDjCols - 1) / ss::kDjCols)), ss::kDjThreads, ss::kDjSmem,
+                               s>>>(w);
     if ((st = launch_status()) != SS_OK)
         return st;
     w.pass = 2;
@@ -347,7 +349,7 @@ int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, in
         return 0;
     // the states of the segments, when the sequence is cut (few heads: they are small)
     const int64_t segs = delta_segments(heads, (dv + 127) / 128, chunks);
-    return segs == 1 ? n : n + heads * 4 * dk * ((segs - 1) * dv + (segs - 2) * dk);
+    return segs == 1 ? n : n + heads * 4 * (dk * ((segs - 1) * dv + (segs - 2) * dk) + (segs - 2));
 }
 
 int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,

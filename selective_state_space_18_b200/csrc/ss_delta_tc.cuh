@@ -37,8 +37,8 @@
 // S -> M S + N, so pass 1 walks every segment but the last for N, its end state from zero
 // (the first from h0), and every one but the first and the last for M, its end state from
 // the identity with v = 0; ss_delta_join_kernel chains them in fp32, and pass 2 walks every
-// segment from its entering state with outputs.  That is the work of three walks in the
-// time of two segments.
+// segment from its entering state with outputs.  A segment whose decays underflow has an M
+// of exactly 0: its walk ends there, and the join has nothing to multiply.
 //
 // Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
 // state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
@@ -508,6 +508,8 @@ struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kP = kB + 2 * kDcHead; // P
     static constexpr int kBar = kP + kDcMat;
     static constexpr int kTmem = kBar + 144;
+    static constexpr int kAlive = kTmem + 4;  // the walk for M: chunks after which it was not 0
+    static constexpr int kDone = kAlive + 4;  // and whether it has become 0
     static constexpr int kBytes = kBar + 256;
 };
 // two CTAs on an SM: 228 KB, 1 KB of it reserved for each
@@ -521,6 +523,7 @@ struct DeltaWalkArgs {
     int pass;                     // 0, or 1 and 2 (see above)
     float *seg_n;                 // [batch, heads_v, segments - 1, dk, dv]: N, then the state after the segment
     float *seg_m;                 // [batch, heads_v, segments - 2, dk, dk]: M of segments 1 ..
+    int *seg_zero;                // [batch, heads_v, segments - 2]: 1 where M is 0 (and not written)
     const unsigned char *blocks;
     const float *h0;              // nullable
     const float *g;               // nullable; g and reset for the first token
@@ -559,7 +562,7 @@ __device__ __forceinline__ void dw_split2(float2 x, uint32_t &hi, uint32_t &lo)
     lo = pack_bf16x2(r.x, r.y);
 }
 
-__device__ __forceinline__ float2 dw_pair(const uint32_t (&r)[16], int e)
+__device__ __forceinline__ float2 dw_pair(const uint32_t (&r)[8], int e)
 {
     return make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
@@ -578,16 +581,17 @@ __device__ __forceinline__ bool elect_one()
 // The element-wise steps hold tiles of 16 lanes as the warp-wide fragments that
 // tcgen05.ld.16x256b, tcgen05.st.16x128b, ldmatrix and stmatrix share: thread t has rows
 // t / 4 and t / 4 + 8 (x = 0, 1), and of every 8 columns the pair 2 (t % 4), + 1.
-// 32 fp32 columns: r[4 k + 2 x + e] is column 8 k + 2 (t % 4) + e.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16])
+// 16 fp32 columns: r[4 k + 2 x + e] is column 8 k + 2 (t % 4) + e.  (Not 32: eight more
+// registers beside H would spill.)
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
     tmem_ld_wait();
-    tmem_ld_fence(r);
+    // (the registers are only valid once the wait has returned)
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
 // 16 columns of packed pairs, those of 8 k in columns 4 k .. : r[2 k + x]
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8])
@@ -629,6 +633,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
              *bar_kh = bars + 7, *bar_u = bars + 8, *bar_qh = bars + 9, *bar_y = bars + 10, *bar_dh = bars + 11 /* [2] */;
     uint64_t *arr_h = bars + 13, *arr_q = bars + 14, *arr_r = bars + 15, *arr_u = bars + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
+    volatile int *s_alive = reinterpret_cast<int *>(sm + DwSmem::kAlive);
+    volatile int *s_done = reinterpret_cast<int *>(sm + DwSmem::kDone);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const bool issuer = warp == kWarps;
@@ -664,6 +670,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         for (int i = 13; i < 17; ++i)
             mbar_init(bars + i, kWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *s_alive = *s_done = 0;
     }
     if (warp == 0) {
         tmem_alloc(tmem_slot, kDwTmemCols);
@@ -744,6 +751,12 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     break;
                 }
                 tc_fence_after();
+                if (for_m && c > 0 && *s_alive != c) { // 0 from here on
+                    *s_done = 1;
+                    begin(bar_kh);
+                    mbar_arrive(bar_kh);
+                    break;
+                }
                 for (int ks = 0; ks < a.nks; ++ks) {
                     const uint64_t kd = sw128_desc(kb + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024);
                     umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, kd, kIdTok, ks > 0);
@@ -863,6 +876,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         const uint32_t lanes = tmem + (uint32_t(row0) << 16);
         // H[m][k][x]: value column col + 16 m + 8 x, keys 64 cg + 8 k + tc, + 1
         float2 H[MT][8][2];
+        bool zero = false; // M has become 0
         // the state the segment starts from: h0, the state after the segment before it, the
         // identity, or zero
         const float *from = nullptr;
@@ -962,29 +976,28 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 ok = false;
                 break;
             }
+            if (for_m && *s_done) {
+                zero = true;
+                break;
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg;
-                uint32_t r[16], v[2][4] = {};
-                // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
-                if (!for_m) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        ldmatrix_x4_trans(v[j], v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
-                                                               ((row0 & 63) >> 3) + 2 * m + ((ln >> 3) & 1)));
-                }
-                tmem_ld_frag(at, r);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t w[8];
+                for (int j = 0; j < 2; ++j) { // 16 tokens
+                    uint32_t r[8], v[4] = {}, w[8];
+                    // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
+                    if (!for_m)
+                        ldmatrix_x4_trans(v, v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
+                                                                ((row0 & 63) >> 3) + 2 * m + ((ln >> 3) & 1)));
+                    tmem_ld_frag(at + 16 * j, r);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int k = 2 * j + i;
-                        const float2 cv = *reinterpret_cast<const float2 *>(sc + 8 * k);
+                        const float2 cv = *reinterpret_cast<const float2 *>(sc + 16 * j + 8 * i);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t vv = v[j][2 * i + x];
-                            dw_split2(__ffma2_rn(make_float2(-cv.x, -cv.y), dw_pair(r, 2 * k + x),
+                            const uint32_t vv = v[2 * i + x];
+                            dw_split2(__ffma2_rn(make_float2(-cv.x, -cv.y), dw_pair(r, 2 * i + x),
                                                  make_float2(__uint_as_float(vv << 16), __uint_as_float(vv & 0xffff0000u))),
                                       w[2 * i + x], w[4 + 2 * i + x]);
                         }
@@ -1002,23 +1015,22 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + 32 * cg;
-                uint32_t r[16];
-                tmem_ld_frag(at, r);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t w[8], u[4];
+                    uint32_t r[8], w[8], u[4];
+                    tmem_ld_frag(at + 16 * j, r);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int k = 2 * j + i;
-                        const float2 wv = *reinterpret_cast<const float2 *>(sw + 8 * k);
+                        const float2 wv = *reinterpret_cast<const float2 *>(sw + 16 * j + 8 * i);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const float2 uu = dw_pair(r, 2 * k + x);
+                            const float2 uu = dw_pair(r, 2 * i + x);
                             u[2 * i + x] = pack_bf16x2(uu.x, uu.y);
                             dw_split2(__fmul2_rn(wv, uu), w[2 * i + x], w[4 + 2 * i + x]);
                         }
                     }
-                    tmem_st_frag(ml + kDwU + 16 * (2 * cg + j), u);
+                    if (outs)
+                        tmem_st_frag(ml + kDwU + 16 * (2 * cg + j), u);
                     tmem_st_frag(at + 16 * j, w);
                 }
             }
@@ -1032,20 +1044,18 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    uint32_t r[16];
-                    tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg, r);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        uint32_t o[4];
+                        uint32_t r[8], o[4];
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg + 16 * j, r);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int k = 2 * j + i;
-                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 8 * k + tc);
+                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 16 * j + 8 * i + tc);
                             sv.x = em.y == 0.0f ? sv.x : 1.0f;
                             sv.y = em.y == 0.0f ? sv.y : 1.0f;
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * k + x));
+                                const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * i + x));
                                 o[2 * i + x] = pack_bf16x2(y.x, y.y);
                             }
                         }
@@ -1077,29 +1087,43 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                if (4 * cg + 2 * hf < a.nks) {
+            for (int kb = 0; kb < 8; kb += 2) { // 16 keys
+                if (4 * cg + kb / 2 < a.nks) {
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        uint32_t r[16];
-                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 32 * hf, r);
+                        uint32_t r[8];
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 8 * kb, r);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
-                                H[m][4 * hf + k][x] =
-                                    __ffma2_rn(make_float2(em.x, em.x), H[m][4 * hf + k][x], dw_pair(r, 2 * k + x));
-                        store_h(m, 4 * hf);
-                        store_h(m, 4 * hf + 2);
+                                H[m][kb + i][x] =
+                                    __ffma2_rn(make_float2(em.x, em.x), H[m][kb + i][x], dw_pair(r, 2 * i + x));
+                        store_h(m, kb);
                     }
                 }
+            }
+            if (for_m) {
+                bool any = false;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        any = any || H[m][k][0].x != 0.0f || H[m][k][0].y != 0.0f || H[m][k][1].x != 0.0f ||
+                              H[m][k][1].y != 0.0f;
+                if (any) // (NaN counts)
+                    *s_alive = c + 1;
             }
             tmem_st_wait();
             arrive(arr_h);
         }
+        if (for_m && ok && tid == 0)
+            a.seg_zero[bh * (a.segments - 2) + seg - 1] = zero;
         // where the state goes: N or M, or the final state after the last segment
         float *to = nullptr;
-        if (for_m)
+        if (zero)
+            ;
+        else if (for_m)
             to = a.seg_m + (bh * (a.segments - 2) + seg - 1) * a.dk * a.dk;
         else if (a.pass == 1)
             to = a.seg_n + (bh * (a.segments - 1) + seg) * a.dk * a.dv;
@@ -1131,60 +1155,105 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 //
 // seg_n[s] <- M_s seg_n[s - 1] + seg_n[s] for s = 1 .. segments - 2, in order: the states
 // after the segments.  One CTA per head and 16 columns, the running state's columns in
-// shared memory, a row and 8 columns a thread; all fp32.  A few microseconds of latency.
+// shared memory, four rows and columns a thread, M staged in blocks ahead of its use; all
+// fp32.
 
-constexpr int kDjThreads = 256, kDjCols = 16;
+constexpr int kDjThreads = 128, kDjCols = 16, kDjK = 32, kDjStages = 3;
+constexpr int kDjRow = kDjK + 4; // floats between rows of a staged block of M
+constexpr int kDjSmem = (kDjStages * 128 * kDjRow + 128 * kDjCols) * 4;
 
 __global__ void __launch_bounds__(kDjThreads) ss_delta_join_kernel(const DeltaWalkArgs a)
 {
-    __shared__ __align__(16) float st[128][kDjCols];
+    extern __shared__ __align__(16) float dj_sm[];
+    float *st = dj_sm + kDjStages * 128 * kDjRow; // [128][kDjCols]
     const int tiles = (a.dv + kDjCols - 1) / kDjCols;
     const int64_t bh = blockIdx.x / unsigned(tiles);
     const int c0 = int(blockIdx.x % unsigned(tiles)) * kDjCols;
-    const int row = threadIdx.x >> 1, c = 8 * (threadIdx.x & 1);
-    const bool in = row < a.dk && c0 + c < a.dv; // (dv is a multiple of 8)
+    const int row = 4 * (threadIdx.x >> 2), c = 4 * (threadIdx.x & 3);
+    const bool in = row < a.dk && c0 + c < a.dv; // (dk and dv are multiples of 8)
     float *n = a.seg_n + bh * (a.segments - 1) * a.dk * a.dv + int64_t(row) * a.dv + c0 + c;
-    const float *m = a.seg_m + bh * (a.segments - 2) * a.dk * a.dk + int64_t(row) * a.dk;
+    const float *m = a.seg_m + bh * (a.segments - 2) * a.dk * a.dk;
+    const int *zero = a.seg_zero + bh * (a.segments - 2);
     const int64_t nstep = int64_t(a.dk) * a.dv, mstep = int64_t(a.dk) * a.dk;
+    // blocks of 128 rows x 32 columns of the M, one after another through three stages
+    const int per = (a.dk + kDjK - 1) / kDjK, blocks = (a.segments - 2) * per;
+    auto fetch = [&](int i) {
+        if (i < blocks && !zero[i / per]) {
+            const float *src = m + (i / per) * mstep + (i % per) * kDjK;
+            float *dst = dj_sm + (i % kDjStages) * 128 * kDjRow;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        st[row][c + e] = in ? n[e] : 0.0f;
-    __syncthreads();
-    for (int s = 1; s < a.segments - 1; ++s) {
-        n += nstep;
-        float2 acc[4];
+            for (int u = 0; u < 128 * kDjK / 4 / kDjThreads; ++u) {
+                const int e = int(threadIdx.x) + kDjThreads * u, r = e >> 3, k = 4 * (e & 7);
+                const bool ok = r < a.dk && (i % per) * kDjK + k < a.dk;
+                cp_async16(dst + r * kDjRow + k, ok ? src + int64_t(r) * a.dk + k : m, ok);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
+    fetch(1);
+    float2 acc[4][2];
+    auto load_n = [&]() {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc[e] = in ? make_float2(n[2 * e], n[2 * e + 1]) : make_float2(0.0f, 0.0f);
-        if (in) {
-#pragma unroll 2
-            for (int k = 0; k < a.dk; k += 8) { // (dk is a multiple of 8)
-                float f[8];
-                *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(m + k);
-                *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(m + k + 4);
+        for (int r = 0; r < 4; ++r) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (in)
+                v = *reinterpret_cast<const float4 *>(n + int64_t(r) * a.dv);
+            acc[r][0] = make_float2(v.x, v.y), acc[r][1] = make_float2(v.z, v.w);
+        }
+    };
+    auto keep = [&]() { // the running state's columns
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float4 lo = *reinterpret_cast<const float4 *>(&st[k + u][c]);
-                    const float4 hi = *reinterpret_cast<const float4 *>(&st[k + u][c + 4]);
-                    const float2 x = make_float2(f[u], f[u]);
-                    acc[0] = __ffma2_rn(x, make_float2(lo.x, lo.y), acc[0]);
-                    acc[1] = __ffma2_rn(x, make_float2(lo.z, lo.w), acc[1]);
-                    acc[2] = __ffma2_rn(x, make_float2(hi.x, hi.y), acc[2]);
-                    acc[3] = __ffma2_rn(x, make_float2(hi.z, hi.w), acc[3]);
+        for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<float4 *>(st + (row + r) * kDjCols + c) =
+                make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
+    };
+    load_n();
+    keep();
+    for (int i = 0; i < blocks; ++i) {
+        if (i % per == 0) {
+            n += nstep;
+            load_n();
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads(); // this block has landed, and the one before it has been read
+        fetch(i + 2);
+        const bool skip = zero[i / per];
+        if (!skip) {
+            const float *mr = dj_sm + (i % kDjStages) * 128 * kDjRow + row * kDjRow;
+            const float *sr = st + (i % per) * kDjK * kDjCols + c;
+#pragma unroll
+            for (int k = 0; k < kDjK; k += 4) {
+                float f[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 v = *reinterpret_cast<const float4 *>(mr + r * kDjRow + k);
+                    f[r][0] = v.x, f[r][1] = v.y, f[r][2] = v.z, f[r][3] = v.w;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sr + (k + u) * kDjCols);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float2 x = make_float2(f[r][u], f[r][u]);
+                        acc[r][0] = __ffma2_rn(x, make_float2(v.x, v.y), acc[r][0]);
+                        acc[r][1] = __ffma2_rn(x, make_float2(v.z, v.w), acc[r][1]);
+                    }
                 }
             }
         }
-        __syncthreads();
-        if (in) {
+        if (i % per == per - 1) {
+            __syncthreads(); // the state before this segment has been read
+            keep();
+            if (in && !skip) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                st[row][c + 2 * e] = n[2 * e] = acc[e].x;
-                st[row][c + 2 * e + 1] = n[2 * e + 1] = acc[e].y;
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<float4 *>(n + int64_t(r) * a.dv) =
+                        make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
             }
         }
-        __syncthreads();
-        m += mstep;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 } // namespace ss
