@@ -125,52 +125,85 @@ struct DeltaPrepArgs {
 
 // ---- preparation ---------------------------------------------------------------------
 //
-// 128 threads, five CTAs per SM.  Warp w computes rows 16 w .. 16 w + 15 of K K^T and
-// Q K^T with mma.sync (64 x 64 products of a microsecond in all do not repay tensor-memory
-// round trips), only up to the diagonal, scales them by the decays and leaves A and P in
-// shared memory.  T is built from A in place: the inverses of the four 16 x 16 diagonal
-// blocks by substitution, one column a lane, then twice T21 = -T22 (A21 T11) for pairs of
-// blocks in packed fp32, with the intermediate product in the empty block above the
-// diagonal.  (Value heads that share a key head repeat its two products, a tenth of the
-// work: kept in registers over the heads they cost the occupancy that hides the rest.)
+// 128 threads, five CTAs per SM.  Warp w owns rows 16 w .. 16 w + 15: it computes them of
+// K K^T and Q K^T with mma.sync, up to the diagonal (64 x 64 products of a microsecond in
+// all do not repay tensor-memory round trips), scales them by the decays into A, which
+// stays in its registers as fragments, and P, and builds its rows of T = (I + A)^{-1} block
+// by block: the inverse T_ww of its 16 x 16 diagonal block by substitution, one column a
+// lane, and then, j = w - 1 down to 0,
+//   T_wj = -T_ww W,   W = sum_{j <= k < w} A_wk T_kj
+// with mma.sync on tf32 operands split in two (22 bits), which keeps the error of fp32
+// arithmetic.  A product's result fragment is the left operand of the next one as it
+// stands, and the transpose of its right operand (the keys of a step taken in the order
+// 0, 2, 4, 6, 1, 3, 5, 7 on both sides), so W is computed as W^T = sum T_kj^T A_wk^T, and
+// only the T_kj^T pass from warp to warp, through shared memory.  (Value heads that share a
+// key head repeat its two products, a tenth of the work: kept in registers over the heads
+// they cost the occupancy that hides the rest.)
+//
+// The rate of shared memory bounds it: with T built by packed fp32 arithmetic on A in
+// shared memory the kernel took twice as long.
 
 constexpr int kDpThreads = 128;
-constexpr int kDpRow = 136;  // elements between rows of the q and k tiles (272 bytes)
-constexpr int kDpARow = 68;  // floats between rows of A
-struct DeltaPrepSmem {       // A and P take the place of the q and k tiles
+constexpr int kDpRow = 136;   // elements between rows of the q and k tiles (272 bytes)
+constexpr int kDpDRow = 20;   // floats between rows of a diagonal block
+struct DeltaPrepSmem {        // the image, T_kj^T and the diagonal blocks take the place of the tiles
     static constexpr int kK = 0, kQ = kDcChunk * kDpRow * 2;
-    static constexpr int kA = 0, kP = kDcChunk * kDpARow * 4;
+    static constexpr int kImg = 0;                    // T hi, T lo, P
+    static constexpr int kTT = kImg + 3 * kDcMat;     // T_kj^T, k < 3, as fragments: [6 blocks][32 lanes][8]
+    static constexpr int kDiag = kTT + 6 * 1024;      // [4 warps][16][kDpDRow]
     static constexpr int kScal = 2 * kQ; // per token: Gh, Gl, cut count, r, p, beta, r / E, beta r E (64 floats each)
     static constexpr int kBytes = kScal + 8 * 256 + 16;
-    static_assert(kP + kDcMat <= kScal, "A and P inside the tiles");
+    static_assert(kDiag + 4 * 16 * kDpDRow * 4 <= kScal, "inside the tiles");
 };
 
-// NR rows of 4 columns of a product: o[r][0..3] += sum_{k < K} a[(row r) k] b[k][0..3]; a
-// and b point into the A array.
-template <int NR> __device__ __forceinline__ void dp_rows(const float *const (&ar)[NR], const float *b, int K, float2 (&o)[NR][2])
+// A 16 x 16 block as the result fragment of two m16n8 products: f[4 n + 2 x + e] is row
+// t / 4 + 8 x, column 8 n + 2 (t % 4) + e.
+struct DpFrag {
+    float f[8];
+};
+
+__device__ __forceinline__ void mma_1688_tf32(float *d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// d += m n, with n given as its transpose; each operand as its first 11 bits and the rest.
+__device__ __forceinline__ void dp_mul(DpFrag &d, const DpFrag &m, const DpFrag &nt)
+{
+    uint32_t mh[8], ml[8], nh[8], nl[8];
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-        o[r][0] = o[r][1] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < K; k += 4) {
-        float av[NR][4];
+    for (int i = 0; i < 8; ++i) {
+        mh[i] = __float_as_uint(m.f[i]) & 0xffffe000u;
+        ml[i] = __float_as_uint(m.f[i] - __uint_as_float(mh[i]));
+        nh[i] = __float_as_uint(nt.f[i]) & 0xffffe000u;
+        nl[i] = __float_as_uint(nt.f[i] - __uint_as_float(nh[i]));
+    }
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const float4 v = *reinterpret_cast<const float4 *>(ar[r] + k);
-            av[r][0] = v.x, av[r][1] = v.y, av[r][2] = v.z, av[r][3] = v.w;
-        }
+    for (int ks = 0; ks < 2; ++ks) {
+        const uint32_t ah[4] = {mh[4 * ks], mh[4 * ks + 2], mh[4 * ks + 1], mh[4 * ks + 3]};
+        const uint32_t al[4] = {ml[4 * ks], ml[4 * ks + 2], ml[4 * ks + 1], ml[4 * ks + 3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 v = *reinterpret_cast<const float4 *>(b + (k + e) * kDpARow);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float2 x = make_float2(av[r][e], av[r][e]);
-                o[r][0] = __ffma2_rn(x, make_float2(v.x, v.y), o[r][0]);
-                o[r][1] = __ffma2_rn(x, make_float2(v.z, v.w), o[r][1]);
-            }
+        for (int n = 0; n < 2; ++n) {
+            const int i = 4 * ks + 2 * n;
+            mma_1688_tf32(d.f + 4 * n, al, nh[i], nh[i + 1]);
+            mma_1688_tf32(d.f + 4 * n, ah, nl[i], nl[i + 1]);
+            mma_1688_tf32(d.f + 4 * n, ah, nh[i], nh[i + 1]);
         }
     }
+}
+
+// A block of packed pairs (rows 16 i, columns 16 j of a matrix) into its slice of the
+// image: matrix lane / 8 of the four 8 x 8, row lane % 8.
+__device__ __forceinline__ void dp_store_block(uint32_t mat, int i, int j, int lane, const uint32_t (&w)[4])
+{
+    const int row = 16 * i + 8 * ((lane >> 3) & 1) + (lane & 7);
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     mat + uint32_t(dc_elem(row, 16 * j + 8 * (lane >> 4)))),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const DeltaPrepArgs a)
@@ -187,8 +220,7 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
     const int n = int(d.seq - t0 < kDcChunk ? d.seq - t0 : kDcChunk); // tokens of this chunk
     __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(dp_sm + Sm::kK);
     __nv_bfloat16 *sq = reinterpret_cast<__nv_bfloat16 *>(dp_sm + Sm::kQ);
-    float *sA = reinterpret_cast<float *>(dp_sm + Sm::kA);
-    unsigned char *sPm = dp_sm + Sm::kP;
+    const uint32_t img = smem_u32(dp_sm + Sm::kImg);
     float *sGh = reinterpret_cast<float *>(dp_sm + Sm::kScal), *sGl = sGh + 64, *sR = sGh + 192, *sP = sGh + 256,
           *sBeta = sGh + 320, *sF = sGh + 384, *sB = sGh + 448;
     int *sN = reinterpret_cast<int *>(sGh + 128);
@@ -327,34 +359,8 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         }
     }
     __syncthreads();
-    // ---- A and P ---------------------------------------------------------------------
-    if (!direct) {
-        const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
-        const float bi[2] = {sB[i0], sB[i0 + 8]};
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt / 2 <= (warp | 1)) { // (above the diagonal: zeros of the slices of P)
-                const int j = 8 * nt + j0;
-                const float2 f = *reinterpret_cast<const float2 *>(sF + j);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = i0 + 8 * x;
-                    float2 av = __fmul2_rn(f, make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
-                    float2 pv = __fmul2_rn(f, make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
-                    av = __fmul2_rn(make_float2(bi[x], bi[x]), av);
-                    if (nt / 2 >= warp) { // on or above the diagonal blocks
-                        av.x = j < i ? av.x : 0.0f;
-                        av.y = j + 1 < i ? av.y : 0.0f;
-                        pv.x = j <= i ? pv.x : 0.0f;
-                        pv.y = j + 1 <= i ? pv.y : 0.0f;
-                    }
-                    if (nt / 2 <= warp)
-                        *reinterpret_cast<float2 *>(sA + i * kDpARow + j) = av;
-                    *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) = pack_bf16x2(pv.x, pv.y);
-                }
-            }
-        }
-    } else {
+    // ---- A, in place of K K^T, and P ---------------------------------------------------
+    {
         const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
         float gih[2], gil[2], bi[2], pi[2];
         int ni[2];
@@ -362,39 +368,64 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         for (int x = 0; x < 2; ++x) {
             const int i = i0 + 8 * x;
             gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
-            bi[x] = sBeta[i] * sR[i];
-            pi[x] = sP[i];
+            bi[x] = direct ? sBeta[i] * sR[i] : sB[i];
+            pi[x] = direct ? sP[i] : 1.0f;
         }
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt / 2 <= (warp | 1)) {
-                const int j = 8 * nt + j0;
-                const float2 gjh = *reinterpret_cast<const float2 *>(sGh + j);
-                const float2 gjl = *reinterpret_cast<const float2 *>(sGl + j);
-                const int2 nj = *reinterpret_cast<const int2 *>(sN + j);
-                const float2 rj = *reinterpret_cast<const float2 *>(sR + j);
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb <= (warp | 1)) { // (above the diagonal: zeros of the slices)
+                uint32_t w[4];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = i0 + 8 * x;
-                    const float dx = j <= i && nj.x == ni[x] ? rj.x * ex2((gih[x] - gjh.x) + (gil[x] - gjl.x)) : 0.0f;
-                    const float dy = j + 1 <= i && nj.y == ni[x] ? rj.y * ex2((gih[x] - gjh.y) + (gil[x] - gjl.y))
-                                                                 : 0.0f;
-                    if (nt / 2 <= warp)
-                        *reinterpret_cast<float2 *>(sA + i * kDpARow + j) =
-                            make_float2(j < i ? bi[x] * dx * kk[nt][2 * x] : 0.0f,
-                                        j + 1 < i ? bi[x] * dy * kk[nt][2 * x + 1] : 0.0f);
-                    *reinterpret_cast<uint32_t *>(sPm + dc_elem(i, j)) =
-                        pack_bf16x2(pi[x] * dx * qk[nt][2 * x], pi[x] * dy * qk[nt][2 * x + 1]);
+                for (int n = 0; n < 2; ++n) {
+                    const int nt = 2 * jb + n, j = 8 * nt + j0;
+                    const float2 f = *reinterpret_cast<const float2 *>(sF + j);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int i = i0 + 8 * x;
+                        float2 d2 = f;
+                        if (direct) {
+                            d2.x = sN[j] == ni[x] ? sR[j] * ex2((gih[x] - sGh[j]) + (gil[x] - sGl[j])) : 0.0f;
+                            d2.y = sN[j + 1] == ni[x] ? sR[j + 1] * ex2((gih[x] - sGh[j + 1]) + (gil[x] - sGl[j + 1])) : 0.0f;
+                        }
+                        float2 av = __fmul2_rn(d2, make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
+                        float2 pv = __fmul2_rn(d2, make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
+                        av = __fmul2_rn(make_float2(bi[x], bi[x]), av);
+                        if (direct)
+                            pv = __fmul2_rn(make_float2(pi[x], pi[x]), pv);
+                        if (jb >= warp) { // on or above the diagonal blocks
+                            av.x = j < i ? av.x : 0.0f;
+                            av.y = j + 1 < i ? av.y : 0.0f;
+                            pv.x = j <= i ? pv.x : 0.0f;
+                            pv.y = j + 1 <= i ? pv.y : 0.0f;
+                        }
+                        kk[nt][2 * x] = av.x;
+                        kk[nt][2 * x + 1] = av.y;
+                        w[2 * n + x] = pack_bf16x2(pv.x, pv.y);
+                    }
                 }
+                dp_store_block(img + 2 * kDcMat, warp, jb, lane, w);
             }
         }
     }
-    __syncwarp();
-    // ---- T -------------------------------------------------------------------------------
-    // the diagonal block of this warp: lane j solves (I + A) x = e_j (both half warps the
-    // same columns)
+    // ---- T ---------------------------------------------------------------------------------
+    float *sD = reinterpret_cast<float *>(dp_sm + Sm::kDiag) + warp * 16 * kDpDRow;
+    float4 *sT = reinterpret_cast<float4 *>(dp_sm + Sm::kTT); // block k (k + 1) / 2 + j, then [lane][2]
+    const int g = lane >> 2, t2 = 2 * (lane & 3);
+    DpFrag tw; // T_ww
     {
-        float *blkA = sA + 16 * warp * (kDpARow + 1);
+        // the diagonal block by rows in shared memory; lane j (and j + 16) solves (I + A) x = e_j
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w == warp) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *reinterpret_cast<float2 *>(sD + (g + 8 * x) * kDpDRow + 8 * n + t2) =
+                            make_float2(kk[2 * w + n][2 * x], kk[2 * w + n][2 * x + 1]);
+            }
+        }
+        __syncwarp();
         float x[16];
         const int j = lane & 15;
 #pragma unroll
@@ -403,7 +434,7 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
 #pragma unroll
         for (int i = 1; i < 16; ++i) {
             float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-            const float4 *row = reinterpret_cast<const float4 *>(blkA + i * kDpARow);
+            const float4 *row = reinterpret_cast<const float4 *>(sD + i * kDpDRow);
 #pragma unroll
             for (int m = 0; m < (i + 3) / 4; ++m) { // A is 0 on and above the diagonal
                 const float4 v = row[m];
@@ -413,73 +444,95 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
             x[i] -= (s0.x + s0.y) + (s1.x + s1.y);
         }
         __syncwarp();
+        // column j as row j: the transpose
         if (lane < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                blkA[i * kDpARow + j] = x[i];
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4 *>(sD + j * kDpDRow + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+        __syncwarp();
+        DpFrag tt;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int xx = 0; xx < 2; ++xx) {
+                const float2 v = *reinterpret_cast<const float2 *>(sD + (g + 8 * xx) * kDpDRow + 8 * n + t2);
+                tt.f[4 * n + 2 * xx] = v.x;
+                tt.f[4 * n + 2 * xx + 1] = v.y;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    tw.f[4 * n + 2 * xx + e] = sD[(8 * n + t2 + e) * kDpDRow + g + 8 * xx];
+            }
+        if (warp < 3) {
+            float4 *dst = sT + (warp * (warp + 1) / 2 + warp) * 64 + lane;
+            dst[0] = make_float4(tt.f[0], tt.f[1], tt.f[2], tt.f[3]);
+            dst[32] = make_float4(tt.f[4], tt.f[5], tt.f[6], tt.f[7]);
         }
     }
-    __syncthreads();
-    // pairs of 16 x 16 blocks: two warps each, one row of four columns a thread
-    {
-        float *base = sA + 32 * (warp >> 1) * (kDpARow + 1); // the pair's top left corner
-        const int i = (tid & 63) >> 2, c = 4 * (tid & 3);
-        float2 o[1][2];
-        const float *const a21[1] = {base + (16 + i) * kDpARow};
-        dp_rows<1>(a21, base + c, 16, o);
-        *reinterpret_cast<float4 *>(base + i * kDpARow + 16 + c) = make_float4(o[0][0].x, o[0][0].y, o[0][1].x, o[0][1].y);
-        __syncthreads();
-        const float *const t22[1] = {base + (16 + i) * kDpARow + 16};
-        dp_rows<1>(t22, base + 16 + c, 16, o);
-        *reinterpret_cast<float4 *>(base + (16 + i) * kDpARow + c) =
-            make_float4(-o[0][0].x, -o[0][0].y, -o[0][1].x, -o[0][1].y);
-    }
-    __syncthreads();
-    // the pair of 32 x 32 blocks: two rows of four columns a thread (the blocks above the
-    // diagonal 16 x 16 blocks hold leftovers and are skipped: T11's right half starts at
-    // row 16, T22's upper half ends at column 16)
-    {
-        const int right = warp >> 1; // A21 T11: the left or the right 16 columns
-        int i = (tid & 63) >> 2, c = 16 * right + 4 * (tid & 3);
-        float2 o[2][2];
-        const float *const a21[2] = {sA + (32 + i) * kDpARow + 16 * right, sA + (48 + i) * kDpARow + 16 * right};
-        dp_rows<2>(a21, sA + 16 * right * kDpARow + c, 32 - 16 * right, o);
+    // T_wj diag(beta), split, into the image
+    auto put = [&](int jb, const DpFrag &t) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<float4 *>(sA + (i + 16 * r) * kDpARow + 32 + c) =
-                make_float4(o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y);
-        __syncthreads();
-        const int low = warp >> 1; // T22 W: the upper or the lower 16 rows
-        i = 16 * low + 2 * ((tid & 63) >> 3);
-        c = 4 * (tid & 7);
-        const float *const t22[2] = {sA + (32 + i) * kDpARow + 32, sA + (33 + i) * kDpARow + 32};
-        dp_rows<2>(t22, sA + 32 + c, 16 + 16 * low, o);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<float4 *>(sA + (32 + i + r) * kDpARow + c) =
-                make_float4(-o[r][0].x, -o[r][0].y, -o[r][1].x, -o[r][1].y);
-    }
-    __syncthreads();
-    // ---- the block: T diag(beta) split, and P, in 16-byte pieces ----------------------
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-        const int e = tid + kDpThreads * u; // piece: rows of 2, slices of 64, 64, 32, 32 rows
-        const int ks = e < 256 ? e >> 7 : 2 + ((e - 256) >> 6);
-        const int r = (e >> 1) & (e < 256 ? 63 : 31), i = r + (ks & 2) * 16, j = 16 * ks + 8 * (e & 1);
-        const int o = dc_elem(i, j);
-        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-        if (i >= 16 * ks) {
+        for (int n = 0; n < 2; ++n) {
+            const float2 bj = *reinterpret_cast<const float2 *>(sBeta + 16 * jb + 8 * n + t2);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float4 t = *reinterpret_cast<const float4 *>(sA + i * kDpARow + j + 4 * x);
-                const float4 bj = *reinterpret_cast<const float4 *>(sBeta + j + 4 * x);
-                split_bf16x2(t.x * bj.x, t.y * bj.y, hi[2 * x], lo[2 * x]);
-                split_bf16x2(t.z * bj.z, t.w * bj.w, hi[2 * x + 1], lo[2 * x + 1]);
+                const float2 v = __fmul2_rn(bj, make_float2(t.f[4 * n + 2 * x], t.f[4 * n + 2 * x + 1]));
+                split_bf16x2(v.x, v.y, hi[2 * n + x], lo[2 * n + x]);
             }
         }
-        *reinterpret_cast<uint4 *>(blk + kDcThi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(blk + kDcTlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4 *>(blk + kDcP + 16 * e) = *reinterpret_cast<const uint4 *>(sPm + 16 * e);
+        dp_store_block(img, warp, jb, lane, hi);
+        dp_store_block(img + kDcMat, warp, jb, lane, lo);
+    };
+    put(warp, tw);
+    if (!(warp & 1)) { // the block above the diagonal one in the slices: zeros
+        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+        dp_store_block(img, warp, warp + 1, lane, zero);
+        dp_store_block(img + kDcMat, warp, warp + 1, lane, zero);
+    }
+#pragma unroll
+    for (int step = 1; step < 4; ++step) {
+        __syncthreads(); // the T_kj^T with k - j < step are there
+        if (warp >= step) {
+            const int j = warp - step;
+            DpFrag wt = {};
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (k >= j && k < warp) {
+                    const float4 *src = sT + (k * (k + 1) / 2 + j) * 64 + lane;
+                    const float4 u = src[0], v = src[32];
+                    const DpFrag tt = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
+                    const DpFrag ak = {{kk[2 * k][0], kk[2 * k][1], kk[2 * k][2], kk[2 * k][3], kk[2 * k + 1][0],
+                                        kk[2 * k + 1][1], kk[2 * k + 1][2], kk[2 * k + 1][3]}};
+                    dp_mul(wt, tt, ak);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                wt.f[i] = -wt.f[i];
+            DpFrag x = {};
+            dp_mul(x, tw, wt);
+            put(j, x);
+            if (warp < 3) {
+                DpFrag xt = {};
+                dp_mul(xt, wt, tw);
+                float4 *dst = sT + (warp * (warp + 1) / 2 + j) * 64 + lane;
+                dst[0] = make_float4(xt.f[0], xt.f[1], xt.f[2], xt.f[3]);
+                dst[32] = make_float4(xt.f[4], xt.f[5], xt.f[6], xt.f[7]);
+            }
+        }
+    }
+    // ---- the matrices of the block ------------------------------------------------------
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(blk + kDcThi), "r"(img),
+                     "r"(2 * kDcMat)
+                     : "memory");
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(blk + kDcP),
+                     "r"(img + 2 * kDcMat), "r"(kDcMat)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
 
