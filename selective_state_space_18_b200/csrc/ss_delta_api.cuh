@@ -70,11 +70,11 @@ template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_
 // ---- the chunked form ----------------------------------------------------------------
 
 // Shapes the chunked form takes (bf16; q, k and v as rows of whole 16-byte vectors, which
-// TMA asks for).  Prompts of up to 16 tokens are walked token by token in less time than
+// TMA asks for; keys of 8 would leave seven eighths of the tiles empty).  Prompts of up to 16 tokens are walked token by token in less time than
 // the two launches take.
 bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_dtype_t dtype)
 {
-    return dtype == SS_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && seq > 16 && seq < (int64_t(1) << 31) - 64 &&
+    return dtype == SS_BF16 && dk >= 16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && seq > 16 && seq < (int64_t(1) << 31) - 64 &&
            batch < (int64_t(1) << 31);
 }
 

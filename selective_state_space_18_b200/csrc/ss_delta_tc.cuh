@@ -170,27 +170,34 @@ __device__ __forceinline__ void mma_1688_tf32(float *d, const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// d += m n, with n given as its transpose; each operand as its first 11 bits and the rest.
-__device__ __forceinline__ void dp_mul(DpFrag &d, const DpFrag &m, const DpFrag &nt)
+// A block as an operand: the first 11 bits of each element and the rest.
+struct DpOp {
+    uint32_t h[8], l[8];
+};
+__device__ __forceinline__ DpOp dp_split(const DpFrag &m)
 {
-    uint32_t mh[8], ml[8], nh[8], nl[8];
+    DpOp o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        mh[i] = __float_as_uint(m.f[i]) & 0xffffe000u;
-        ml[i] = __float_as_uint(m.f[i] - __uint_as_float(mh[i]));
-        nh[i] = __float_as_uint(nt.f[i]) & 0xffffe000u;
-        nl[i] = __float_as_uint(nt.f[i] - __uint_as_float(nh[i]));
+        o.h[i] = __float_as_uint(m.f[i]) & 0xffffe000u;
+        o.l[i] = __float_as_uint(m.f[i] - __uint_as_float(o.h[i]));
     }
+    return o;
+}
+
+// d += m n, with n given as its transpose.
+__device__ __forceinline__ void dp_mul(DpFrag &d, const DpOp &m, const DpOp &nt)
+{
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-        const uint32_t ah[4] = {mh[4 * ks], mh[4 * ks + 2], mh[4 * ks + 1], mh[4 * ks + 3]};
-        const uint32_t al[4] = {ml[4 * ks], ml[4 * ks + 2], ml[4 * ks + 1], ml[4 * ks + 3]};
+        const uint32_t ah[4] = {m.h[4 * ks], m.h[4 * ks + 2], m.h[4 * ks + 1], m.h[4 * ks + 3]};
+        const uint32_t al[4] = {m.l[4 * ks], m.l[4 * ks + 2], m.l[4 * ks + 1], m.l[4 * ks + 3]};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const int i = 4 * ks + 2 * n;
-            mma_1688_tf32(d.f + 4 * n, al, nh[i], nh[i + 1]);
-            mma_1688_tf32(d.f + 4 * n, ah, nl[i], nl[i + 1]);
-            mma_1688_tf32(d.f + 4 * n, ah, nh[i], nh[i + 1]);
+            mma_1688_tf32(d.f + 4 * n, al, nt.h[i], nt.h[i + 1]);
+            mma_1688_tf32(d.f + 4 * n, ah, nt.l[i], nt.l[i + 1]);
+            mma_1688_tf32(d.f + 4 * n, ah, nt.h[i], nt.h[i + 1]);
         }
     }
 }
@@ -362,49 +369,51 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
     // ---- A, in place of K K^T, and P ---------------------------------------------------
     {
         const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
-        float gih[2], gil[2], bi[2], pi[2];
-        int ni[2];
+        // rows scale by bi (A) and pi (P); d2(j, x) are the factors of columns j and j + 1
+        auto scale = [&](float2 bi, float2 pi, auto d2) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = i0 + 8 * x;
-            gih[x] = sGh[i], gil[x] = sGl[i], ni[x] = sN[i];
-            bi[x] = direct ? sBeta[i] * sR[i] : sB[i];
-            pi[x] = direct ? sP[i] : 1.0f;
-        }
+            for (int jb = 0; jb < 4; ++jb) {
+                if (jb <= (warp | 1)) { // (above the diagonal: zeros of the slices)
+                    uint32_t w[4];
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            if (jb <= (warp | 1)) { // (above the diagonal: zeros of the slices)
-                uint32_t w[4];
+                    for (int n = 0; n < 2; ++n) {
+                        const int nt = 2 * jb + n, j = 8 * nt + j0;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int nt = 2 * jb + n, j = 8 * nt + j0;
-                    const float2 f = *reinterpret_cast<const float2 *>(sF + j);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int i = i0 + 8 * x;
-                        float2 d2 = f;
-                        if (direct) {
-                            d2.x = sN[j] == ni[x] ? sR[j] * ex2((gih[x] - sGh[j]) + (gil[x] - sGl[j])) : 0.0f;
-                            d2.y = sN[j + 1] == ni[x] ? sR[j + 1] * ex2((gih[x] - sGh[j + 1]) + (gil[x] - sGl[j + 1])) : 0.0f;
+                        for (int x = 0; x < 2; ++x) {
+                            const int i = i0 + 8 * x;
+                            const float b1 = x ? bi.y : bi.x, p1 = x ? pi.y : pi.x;
+                            const float2 f = d2(j, x);
+                            float2 av = __fmul2_rn(__fmul2_rn(f, make_float2(b1, b1)),
+                                                   make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
+                            float2 pv = __fmul2_rn(__fmul2_rn(f, make_float2(p1, p1)),
+                                                   make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
+                            if (jb >= warp) { // on or above the diagonal blocks
+                                av.x = j < i ? av.x : 0.0f;
+                                av.y = j + 1 < i ? av.y : 0.0f;
+                                pv.x = j <= i ? pv.x : 0.0f;
+                                pv.y = j + 1 <= i ? pv.y : 0.0f;
+                            }
+                            kk[nt][2 * x] = av.x;
+                            kk[nt][2 * x + 1] = av.y;
+                            w[2 * n + x] = pack_bf16x2(pv.x, pv.y);
                         }
-                        float2 av = __fmul2_rn(d2, make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
-                        float2 pv = __fmul2_rn(d2, make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
-                        av = __fmul2_rn(make_float2(bi[x], bi[x]), av);
-                        if (direct)
-                            pv = __fmul2_rn(make_float2(pi[x], pi[x]), pv);
-                        if (jb >= warp) { // on or above the diagonal blocks
-                            av.x = j < i ? av.x : 0.0f;
-                            av.y = j + 1 < i ? av.y : 0.0f;
-                            pv.x = j <= i ? pv.x : 0.0f;
-                            pv.y = j + 1 <= i ? pv.y : 0.0f;
-                        }
-                        kk[nt][2 * x] = av.x;
-                        kk[nt][2 * x + 1] = av.y;
-                        w[2 * n + x] = pack_bf16x2(pv.x, pv.y);
                     }
+                    dp_store_block(img + 2 * kDcMat, warp, jb, lane, w);
                 }
-                dp_store_block(img + 2 * kDcMat, warp, jb, lane, w);
             }
+        };
+        if (!direct) {
+            scale(make_float2(sB[i0], sB[i0 + 8]), make_float2(1.0f, 1.0f),
+                  [&](int j, int) { return *reinterpret_cast<const float2 *>(sF + j); });
+        } else {
+            const float gih[2] = {sGh[i0], sGh[i0 + 8]}, gil[2] = {sGl[i0], sGl[i0 + 8]};
+            const int ni[2] = {sN[i0], sN[i0 + 8]};
+            scale(make_float2(sBeta[i0] * sR[i0], sBeta[i0 + 8] * sR[i0 + 8]), make_float2(sP[i0], sP[i0 + 8]),
+                  [&](int j, int x) {
+                      return make_float2(
+                          sN[j] == ni[x] ? sR[j] * ex2((gih[x] - sGh[j]) + (gil[x] - sGl[j])) : 0.0f,
+                          sN[j + 1] == ni[x] ? sR[j + 1] * ex2((gih[x] - sGh[j + 1]) + (gil[x] - sGl[j + 1])) : 0.0f);
+                  });
         }
     }
     // ---- T ---------------------------------------------------------------------------------
@@ -485,6 +494,7 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         dp_store_block(img + kDcMat, warp, jb, lane, lo);
     };
     put(warp, tw);
+    const DpOp to = dp_split(tw);
     if (!(warp & 1)) { // the block above the diagonal one in the slices: zeros
         const uint32_t zero[4] = {0u, 0u, 0u, 0u};
         dp_store_block(img, warp, warp + 1, lane, zero);
@@ -504,18 +514,19 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
                     const DpFrag tt = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
                     const DpFrag ak = {{kk[2 * k][0], kk[2 * k][1], kk[2 * k][2], kk[2 * k][3], kk[2 * k + 1][0],
                                         kk[2 * k + 1][1], kk[2 * k + 1][2], kk[2 * k + 1][3]}};
-                    dp_mul(wt, tt, ak);
+                    dp_mul(wt, dp_split(tt), dp_split(ak));
                 }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 wt.f[i] = -wt.f[i];
+            const DpOp wo = dp_split(wt);
             DpFrag x = {};
-            dp_mul(x, tw, wt);
+            dp_mul(x, to, wo);
             put(j, x);
             if (warp < 3) {
                 DpFrag xt = {};
-                dp_mul(xt, wt, tw);
+                dp_mul(xt, wo, to);
                 float4 *dst = sT + (warp * (warp + 1) / 2 + j) * 64 + lane;
                 dst[0] = make_float4(xt.f[0], xt.f[1], xt.f[2], xt.f[3]);
                 dst[32] = make_float4(xt.f[4], xt.f[5], xt.f[6], xt.f[7]);

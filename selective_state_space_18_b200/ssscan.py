@@ -686,37 +686,29 @@ def ss_join_segments(composites, rank=None, *, carry=None, final_state=None, wan
     return carry, final_state
 
 
-def _on_launch_stream(fn):
+def _elsewhere(fn, first, stream, *args, **kwargs):
     """Run a wrapper with its first tensor's device current and, when ``stream`` is given,
     on that stream: the copies, outputs and workspaces that the wrapper makes then belong
     to the stream the kernels run on, so nothing of theirs is reused before they end."""
-    lead = fn.__code__.co_varnames[0]
-
-    @functools.wraps(fn)
-    def wrapper(*args, stream=None, **kwargs):
-        first = args[0] if args else kwargs[lead]
-        index = first.get_device()
-        if index < 0:
-            raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
-        if stream is None:
-            if torch.cuda.current_device() == index:
-                return fn(*args, **kwargs)
-            with torch.cuda.device(index):
-                return fn(*args, **kwargs)
-        if stream.device != first.device:
-            raise ValueError(f"stream is on {stream.device}, expected {first.device}")
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return wrapper
+    if not first.is_cuda:
+        raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return fn(first, *args, **kwargs)
+    if stream.device != first.device:
+        raise ValueError(f"stream is on {stream.device}, expected {first.device}")
+    with torch.cuda.stream(stream):
+        return fn(first, *args, **kwargs)
 
 
 def _check(t, name, index, dtype, shape):
+    if t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        return
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected device {index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _rows_of(t, name, index, dtype, shape):
@@ -741,13 +733,9 @@ def _rows_of(t, name, index, dtype, shape):
 
 
 def _dense(t, name, index, dtype, shape):
-    """An optional tensor as (tensor or None, address or None), copied when not contiguous."""
-    if t is None:
-        return None, None
+    """A tensor that the library reads as contiguous: itself, or a copy."""
     _check(t, name, index, dtype, shape)
-    if not t.is_contiguous():
-        t = t.contiguous()
-    return t, t.data_ptr()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _dense_out(t, name, index, dtype, shape):
@@ -773,9 +761,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-@_on_launch_stream
 def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None, qk_l2norm=False, outputs=None,
-                  final_state=None, return_final_state=True, workspace=True):
+                  final_state=None, return_final_state=True, workspace=True, stream=None):
     """Gated delta rule over a prompt: S_t = e^g_t S_{t-1} + k_t u_t^T with u_t = beta_t
     (v_t - e^g_t S_{t-1}^T k_t), outputs_t = scale S_t^T q_t.  q, k: [batch, seq, heads_k,
     dk]; v: [batch, seq, heads_v, dv] (float32 or bfloat16, slices of one projection are
@@ -788,34 +775,47 @@ def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None
     workspace: True (allocated for the call), False (none: the token-by-token kernel) or a
     uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself."""
     index, dt = q.get_device(), q.dtype
+    if stream is not None or index < 0 or index != torch.cuda.current_device():
+        return _elsewhere(ss_delta_scan, q, stream, k, v, g, beta, reset=reset, h0=h0, scale=scale,
+                          qk_l2norm=qk_l2norm, outputs=outputs, final_state=final_state,
+                          return_final_state=return_final_state, workspace=workspace)
     code = _dtype_code(q)
     hk, hv, dk, dv = _delta_sizes("ss_delta_scan", q, v, 2)
     bt, L = q.shape[:2]
     q, qs = _rows_of(q, "q", index, dt, (bt, L, hk, dk))
     k, ks = _rows_of(k, "k", index, dt, (bt, L, hk, dk))
     v, vs = _rows_of(v, "v", index, dt, (bt, L, hv, dv))
-    g, pg = _dense(g, "g", index, torch.float32, (bt, L, hv))
-    beta, pb = _dense(beta, "beta", index, torch.float32, (bt, L, hv))
-    h0, ph = _dense(h0, "h0", index, torch.float32, (bt, hv, dk, dv))
-    pr = None
+    pg = pb = ph = pr = pf = pw = None
+    nw = 0
+    if g is not None:
+        g = _dense(g, "g", index, torch.float32, (bt, L, hv))
+        pg = g.data_ptr()
+    if beta is not None:
+        beta = _dense(beta, "beta", index, torch.float32, (bt, L, hv))
+        pb = beta.data_ptr()
+    if h0 is not None:
+        h0 = _dense(h0, "h0", index, torch.float32, (bt, hv, dk, dv))
+        ph = h0.data_ptr()
     if reset is not None:
         if reset.dtype != torch.bool and reset.dtype != torch.uint8:
             raise TypeError("reset must be bool or uint8")
-        reset, pr = _dense(reset, "reset", index, reset.dtype, (bt, L))
+        reset = _dense(reset, "reset", index, reset.dtype, (bt, L))
+        pr = reset.data_ptr()
     if outputs is None:
-        outputs = q.new_empty((bt, L, hv, dv))
+        outputs = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _dense_out(outputs, "outputs", index, dt, (bt, L, hv, dv))
     if final_state is not None:
         _dense_out(final_state, "final_state", index, torch.float32, (bt, hv, dk, dv))
+        pf = final_state.data_ptr()
     elif return_final_state:
-        final_state = q.new_empty((bt, hv, dk, dv), dtype=torch.float32)
+        final_state = torch.empty((bt, hv, dk, dv), dtype=torch.float32, device=q.device)
+        pf = final_state.data_ptr()
     lib = load_library()
-    pw, nw = None, 0
     if workspace is True:
         nw = lib.ss_delta_workspace_bytes(bt, L, hk, hv, dk, dv, code)
         if nw:
-            workspace = q.new_empty(nw, dtype=torch.uint8)
+            workspace = torch.empty(nw, dtype=torch.uint8, device=q.device)
             pw = workspace.data_ptr()
     elif workspace is not None and workspace is not False:
         if workspace.get_device() != index or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -823,8 +823,7 @@ def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None
         pw, nw = workspace.data_ptr(), workspace.numel()
     st = lib.ss_delta_scan(bt, L, hk, hv, dk, dv, code, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, pg, pb,
                            pr, ph, dk ** -0.5 if scale is None else scale, SS_QK_L2NORM if qk_l2norm else 0,
-                           outputs.data_ptr(), None if final_state is None else final_state.data_ptr(), pw, nw,
-                           _raw_stream(index))
+                           outputs.data_ptr(), pf, pw, nw, _raw_stream(index))
     if st != 0:
         raise SSError("ss_delta_scan", st)
     return {"outputs": outputs, "final_state": final_state}
@@ -836,12 +835,13 @@ def ss_delta_workspace_bytes(batch, seq, heads_k, heads_v, dk, dv, dtype=torch.b
                                                        SS_BF16 if dtype == torch.bfloat16 else SS_F32))
 
 
-@_on_launch_stream
-def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=False, y=None):
+def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=False, y=None, stream=None):
     """Decode step of the gated delta rule: ``state`` [batch, heads_v, dk, dv] float32 is
     updated in place by one token.  q, k: [batch, heads_k, dk]; v: [batch, heads_v, dv];
     g, beta: [batch, heads_v] float32 or None.  Returns y [batch, heads_v, dv]."""
     index, dt = state.get_device(), q.dtype
+    if stream is not None or index < 0 or index != torch.cuda.current_device():
+        return _elsewhere(ss_delta_update, state, stream, q, k, v, g, beta, scale=scale, qk_l2norm=qk_l2norm, y=y)
     code = _dtype_code(q)
     hk, hv, dk, dv = _delta_sizes("ss_delta_update", q, v, 1)
     bt = q.shape[0]
@@ -850,10 +850,15 @@ def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=
     q, qs = _rows_of(q, "q", index, dt, (bt, hk, dk))
     k, ks = _rows_of(k, "k", index, dt, (bt, hk, dk))
     v, vs = _rows_of(v, "v", index, dt, (bt, hv, dv))
-    g, pg = _dense(g, "g", index, torch.float32, (bt, hv))
-    beta, pb = _dense(beta, "beta", index, torch.float32, (bt, hv))
+    pg = pb = None
+    if g is not None:
+        g = _dense(g, "g", index, torch.float32, (bt, hv))
+        pg = g.data_ptr()
+    if beta is not None:
+        beta = _dense(beta, "beta", index, torch.float32, (bt, hv))
+        pb = beta.data_ptr()
     if y is None:
-        y = q.new_empty((bt, hv, dv))
+        y = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _dense_out(y, "y", index, dt, (bt, hv, dv))
     st = load_library().ss_delta_update(bt, hk, hv, dk, dv, code, state.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
@@ -864,9 +869,8 @@ def ss_delta_update(state, q, k, v, g=None, beta=None, *, scale=None, qk_l2norm=
     return y
 
 
-@_on_launch_stream
 def ss_group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=False, center=True, activation=None,
-                  eps=1e-5, y=None):
+                  eps=1e-5, y=None, stream=None):
     """Group norm over the last dimension: per row and group of channels // groups
     consecutive channels, (x - mean) / sqrt(var + eps) (without the mean when ``center``
     is false), times ``weight`` plus ``bias``, then SiLU (activation="silu"), then times
@@ -874,6 +878,9 @@ def ss_group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=Fa
     x, gate, y: [..., channels] float32 or bfloat16; weight, bias: float32 [channels], or
     [channels // groups] for one set shared by all groups (both alike)."""
     index, dt = x.get_device(), x.dtype
+    if stream is not None or index < 0 or index != torch.cuda.current_device():
+        return _elsewhere(ss_group_norm, x, stream, groups, weight, bias, gate=gate, gate_first=gate_first,
+                          center=center, activation=activation, eps=eps, y=y)
     code = _dtype_code(x)
     if x.dim() < 1:
         raise ValueError("x must have a channel dimension")
@@ -897,10 +904,17 @@ def ss_group_norm(x, groups, weight=None, bias=None, *, gate=None, gate_first=Fa
     if first is not None and groups > 1 and first.shape == (size,):
         width = (size,)
         flags |= SS_NORM_SHARED
-    weight, pwt = _dense(weight, "weight", index, torch.float32, width)
-    bias, pbs = _dense(bias, "bias", index, torch.float32, width)
+    pwt = pbs = None
+    if weight is not None:
+        weight = _dense(weight, "weight", index, torch.float32, width)
+        pwt = weight.data_ptr()
+    if bias is not None:
+        bias = _dense(bias, "bias", index, torch.float32, width)
+        pbs = bias.data_ptr()
     if y is None:
-        y = x.new_empty(shape)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if x.shape != shape:
+            y = y.view(shape)
     else:
         _dense_out(y, "y", index, dt, shape)
     st = load_library().ss_group_norm(x.shape[0], groups, size, code, x.data_ptr(), xs, pz, zs, pwt, pbs, eps, flags,
