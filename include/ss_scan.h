@@ -340,7 +340,8 @@ SS_API int ss_debug_set_scan_two_level(int mode);
  * warps withhold their first "L o S written" arrival, so the issuing warp's wait for it
  * can never be satisfied: the call ends on the wait time limit (shorten it with
  * ss_debug_set_wait_limit) with SS_ERR_TIMEOUT in the status word and no output
- * written (a failure-path test aid: nothing faults, every wait is bounded).  Returns
+ * written (a failure-path test aid: nothing faults, every wait is bounded); the chunked
+ * form of ss_delta_scan withholds an arrival of its first chunk in the same way.  Returns
  * SS_OK, or SS_ERR_UNSUPPORTED for any other mode.
  */
 SS_API int ss_debug_set_gated_path(int mode);
@@ -407,6 +408,16 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *
  * heads_v must be a multiple of heads_k (SS_ERR_SHAPE), dk at most 256
  * (SS_ERR_UNSUPPORTED).  Inputs must be finite (but for g) where they are read.
+ *
+ * Two forms:
+ *  - bf16 with dk a multiple of 8 from 16 to 128, dv a multiple of 8, more than 16 tokens,
+ *    16-byte aligned tensors, strides that are multiples of 8 and a workspace: chunks of 64
+ *    tokens on the tensor cores.  The state is held in float32 and its operands in 16 bits
+ *    of mantissa (final_state follows float32 arithmetic to about 5e-6 of its size), the
+ *    outputs' last products take bf16 operands.  Few heads and a long sequence are cut into
+ *    segments that run at once;
+ *  - every other case: token by token, all arithmetic in float32.
+ * Results are the same from call to call.
  */
 enum { SS_QK_L2NORM = 4u };
 SS_API int ss_delta_scan(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,

@@ -169,7 +169,10 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     w.segments = (p.nchunks + w.seg_chunks - 1) / w.seg_chunks;
     w.seg_n = reinterpret_cast<float *>(p.blocks + a.batch * a.heads_v * p.nchunks * ss::kDcBlockBytes);
     w.seg_m = w.seg_n + a.batch * a.heads_v * (w.segments - 1) * a.dk * a.dv;
-    w.seg_zero = reinterpret_cast<int *>(w.seg_m + a.batch * a.heads_v * (w.segments - 2) * a.dk * a.dk);
+    float *end_m = w.seg_m + a.batch * a.heads_v * (w.segments - 2) * a.dk * a.dk;
+    w.seg_h0 = a.h0 && a.final_state == a.h0 ? end_m : nullptr;
+    w.seg_zero = reinterpret_cast<int *>(end_m + a.batch * a.heads_v * a.dk * a.dv);
+    w.hold = g_gated_path.load(std::memory_order_relaxed) == 3 ? 1 : 0;
     w.h0 = a.h0;
     w.g = a.g;
     w.reset = a.reset;
@@ -349,7 +352,7 @@ int64_t ss_delta_workspace_bytes(int64_t batch, int64_t seq, int64_t heads_k, in
         return 0;
     // the states of the segments, when the sequence is cut (few heads: they are small)
     const int64_t segs = delta_segments(heads, (dv + 127) / 128, chunks);
-    return segs == 1 ? n : n + heads * 4 * (dk * ((segs - 1) * dv + (segs - 2) * dk) + (segs - 2));
+    return segs == 1 ? n : n + heads * 4 * (dk * (segs * dv + (segs - 2) * dk) + (segs - 2));
 }
 
 int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv, ss_dtype_t dtype,

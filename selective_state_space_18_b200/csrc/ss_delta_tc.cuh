@@ -586,8 +586,11 @@ struct DeltaWalkArgs {
     int segments, seg_chunks;     // 1 segment: one pass over all chunks
     int pass;                     // 0, or 1 and 2 (see above)
     float *seg_n;                 // [batch, heads_v, segments - 1, dk, dv]: N, then the state after the segment
+    float *seg_h0;                // [batch, heads_v, dk, dv]: pass 1's copy of h0, which pass 2 reads when the
+                                  // final state takes h0's place; null otherwise
     float *seg_m;                 // [batch, heads_v, segments - 2, dk, dk]: M of segments 1 ..
     int *seg_zero;                // [batch, heads_v, segments - 2]: 1 where M is 0 (and not written)
+    int hold;                     // failure-path test aid: withhold the first arrivals on arr_r
     const unsigned char *blocks;
     const float *h0;              // nullable
     const float *g;               // nullable; g and reset for the first token
@@ -947,7 +950,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         if (a.pass == 2 && seg > 0)
             from = a.seg_n + (bh * (a.segments - 1) + seg - 1) * a.dk * a.dv;
         else if (seg == 0 && a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h))
-            from = a.h0 + bh * a.dk * a.dv;
+            from = (a.pass == 2 && a.seg_h0 ? a.seg_h0 : a.h0) + bh * a.dk * a.dv;
         const int64_t sofs = int64_t(64 * cg + tc) * cols + col;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -961,6 +964,10 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     H[m][k][x] = make_float2(in ? from[o] : 0.0f, in ? from[o + cols] : 0.0f);
                     if (for_m) // the identity
                         H[m][k][x] = make_float2(key == vc ? 1.0f : 0.0f, key + 1 == vc ? 1.0f : 0.0f);
+                    if (in && a.pass == 1 && seg == 0 && a.seg_h0) {
+                        a.seg_h0[bh * a.dk * a.dv + o] = H[m][k][x].x;
+                        a.seg_h0[bh * a.dk * a.dv + o + cols] = H[m][k][x].y;
+                    }
                 }
         // 16 keys (2 k-blocks from kb) of tile m as operand columns
         auto store_h = [&](int m, int kb) {
@@ -1070,7 +1077,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
             }
             tmem_st_wait();
-            arrive(arr_r);
+            if (!(a.hold && c == 0))
+                arrive(arr_r);
             // ---- U^T rounded, and w o U over it -----------------------------------------------
             if (!wait(bar_u, ph)) {
                 ok = false;

@@ -176,6 +176,22 @@ def test_chaining_in_place(orc):
     assert_close(state.cpu(), ref["final_state"], TOL[F32], "state")
 
 
+def test_chaining_in_place_over_segments(orc):
+    """The final state in h0's place while the sequence is walked in segments (the first
+    segment's second walk reads h0 after the last one may have written it)."""
+    inp = make_delta_inputs(1, 3000, 1, 4, 128, 128, "bf16", seed=3155, h0=True)
+    inp["g"] = inp["g"] * 1e-2
+    ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
+    d = _cuda_dict(inp)
+    apart = ssscan.ss_delta_scan(**d, scale=1.0, qk_l2norm=True)
+    for _ in range(3):
+        state = d["h0"].clone()
+        out = ssscan.ss_delta_scan(**dict(d, h0=state), final_state=state, scale=1.0, qk_l2norm=True)
+        assert torch.equal(out["outputs"], apart["outputs"]) and torch.equal(state, apart["final_state"])
+    assert_close(out["outputs"].cpu(), ref["outputs"], TOL[BF16], "outputs")
+    assert_close(state.cpu(), ref["final_state"], TOL[F32], "state")
+
+
 def test_supplied_buffers_and_no_final_state():
     inp = _cuda_dict(make_delta_inputs(1, 130, 1, 1, 128, 128, "bf16", seed=3160))
     ref = ssscan.ss_delta_scan(**inp)
@@ -304,3 +320,26 @@ def test_layer_prompt_decode_norm(orc, dtype):
     assert_close(y.cpu(), ref["outputs"].reshape(2, L + n, 512), TOL[y.dtype], "outputs")
     assert_close(state.cpu(), ref["final_state"], TOL[F32], "state")
     assert_close(o.cpu(), orc.group_norm(y.cpu(), 4, w, gate=z, center=False, eps=1e-6), TOL[o.dtype], "norm")
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 1, 2, 128, 128), (1, 1600, 1, 2, 128, 128)])
+def test_timed_out_waits_report_and_recover(shape):
+    """Failure detection without a GPU fault: with an arrival of the first chunk withheld
+    and the wait limit cut to 2 ms, the walk's waits give up, the status word reports
+    SS_ERR_TIMEOUT, and the next call gives the normal answer."""
+    d = _cuda_dict(make_delta_inputs(*shape, "bf16", seed=3500, h0=True))
+    ref = ssscan.ss_delta_scan(**d, qk_l2norm=True)
+    assert ssscan.ss_debug_status() == "SS_OK"
+    ssscan.ss_debug_set_wait_limit(2000)
+    ssscan.ss_debug_set_gated_path(3)
+    try:
+        ssscan.ss_delta_scan(**d, qk_l2norm=True)
+        torch.cuda.synchronize()
+        assert ssscan.ss_debug_status() == "SS_ERR_TIMEOUT"
+    finally:
+        ssscan.ss_debug_set_gated_path(0)
+        ssscan.ss_debug_set_wait_limit(0)
+    out = ssscan.ss_delta_scan(**d, qk_l2norm=True)
+    torch.cuda.synchronize()
+    assert ssscan.ss_debug_status() == "SS_OK"
+    assert torch.equal(out["outputs"], ref["outputs"]) and torch.equal(out["final_state"], ref["final_state"])
