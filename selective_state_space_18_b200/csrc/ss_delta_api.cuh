@@ -78,15 +78,16 @@ bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
            batch < (int64_t(1) << 31);
 }
 
-// Segments of the two-pass walk (1: one pass): as many as make pass 2 fill the GPU with
-// two walks on every SM, three at least and four chunks each at least.  A step of a walk
-// takes 1.4 times as long beside another one, so S segments turn n steps into about
-// (1.4 + 1.2) n / S, or (1.4 + 2.4) n / S where every M has to be walked to the end.
-constexpr int64_t kDeltaWalkSlots = 2 * 148;
+// Segments of the two-pass walk (1: one pass).  Two passes over 1/S of the chunks, with
+// most SMs holding two walks (1.4 times as long a step each), and the join, against one
+// pass: measured on 256 chunks x 32 heads, 0.94 ms in one pass, 0.62, 0.55, 0.55, 0.56 and
+// 0.59 ms with 4, 6, 7, 9 and 12 segments, and nothing gained on 24 chunks x 36 heads (97
+// to 116 us with 4 to 6 segments, 99 us in one pass).
+constexpr int64_t kDeltaWalks = 192; // of pass 2
 int64_t delta_segments(int64_t heads, int64_t tiles, int64_t chunks)
 {
-    int64_t segs = heads > kDeltaWalkSlots ? 1 : kDeltaWalkSlots / (heads * tiles);
-    segs = segs < chunks / 4 ? segs : chunks / 4;
+    int64_t segs = heads > kDeltaWalks ? 1 : kDeltaWalks / (heads * tiles);
+    segs = segs < chunks / 12 ? segs : chunks / 12;
     return segs < 3 ? 1 : segs;
 }
 
@@ -115,15 +116,15 @@ bool encode_heads(CUtensorMap *map, const void *base, int64_t d, int64_t heads, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MT>
+template <int G>
 int launch_delta_walk_t(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps, unsigned grid, uint32_t *status,
                         cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
-    const int st = ensure_smem(ss::ss_delta_walk_kernel<MT>, size_t(ss::DwSmem::kBytes), smem_done);
+    const int st = ensure_smem(ss::ss_delta_walk_kernel<G>, size_t(ss::DwSmem::kBytes), smem_done);
     if (st != SS_OK)
         return st;
-    ss::ss_delta_walk_kernel<MT><<<grid, ss::DwShape<MT>::kThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
+    ss::ss_delta_walk_kernel<G><<<grid, ss::DwShape<G>::kThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
     return launch_status();
 }
 
@@ -136,7 +137,7 @@ int launch_delta_walk(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &maps,
         return SS_ERR_CUDA;
     if (grid > 0x7fffffffLL)
         return SS_ERR_SHAPE;
-    return grid <= sms ? launch_delta_walk_t<1>(w, maps, unsigned(grid), status, s)
+    return grid <= sms ? launch_delta_walk_t<4>(w, maps, unsigned(grid), status, s)
                        : launch_delta_walk_t<2>(w, maps, unsigned(grid), status, s);
 }
 

@@ -549,13 +549,19 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
 
 // ---- the walk ------------------------------------------------------------------------
 
-// MT: tiles of 16 lanes per compute warp, 2 (eight compute warps, two CTAs per SM) or 1
-// (sixteen compute warps, one CTA per SM)
-template <int MT> struct DwShape {
-    static constexpr int kWarps = 16 / MT;           // compute warps
+// G: groups of four compute warps, each with a G-th of the columns: 2 (two CTAs per SM) or
+// 4 (one CTA per SM).  A CTA alone on its SM keeps Y^T of one chunk beside KH^T of the next
+// (D1 alternates between two places), so that the outputs leave after the state is handed
+// on, while the next chunk's first product runs.
+template <int G> struct DwShape {
+    static constexpr int kWarps = 4 * G;              // compute warps
     static constexpr int kThreads = 32 * kWarps + 32; // + the issuer warp
+    static constexpr int kCtas = G == 2 ? 2 : 1;      // per SM
+    static constexpr int kTok = kDcChunk / G, kKeys = 128 / G; // columns of a warp: tokens, keys
+    static constexpr bool kLate = G == 4;
+    static constexpr uint32_t kCols = kLate ? 512 : 256; // tensor memory
+    static constexpr uint32_t kD1Step = kLate ? 128 : 0; // from D1 of even chunks to D1 of odd ones
 };
-constexpr uint32_t kDwTmemCols = 256; // (two CTAs per SM)
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
 // then R^T over it in the same form (16 columns per 16 tokens), then Y^T.  D2: U^T, then
@@ -567,7 +573,7 @@ struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kK = 0;                // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
     static constexpr int kQ = kK + 2 * 16384;   // q chunk: two tiles
     static constexpr int kV = kQ + 16384;       // v chunk: two [64 tokens x 64 values] tiles
-    static constexpr int kY = kV + 16384;       // outputs: tiles of [32 tokens x 32 or 16 values], one per compute warp
+    static constexpr int kY = kV + 16384;       // outputs: a tile of [kTok tokens x 32 values] per compute warp
     static constexpr int kB = kY + 16384;       // workspace blocks up to P: 2 stages
     static constexpr int kP = kB + 2 * kDcHead; // P
     static constexpr int kBar = kP + kDcMat;
@@ -687,11 +693,13 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t
                  : "memory");
 }
 
-template <int MT>
-__global__ void __launch_bounds__(DwShape<MT>::kThreads, MT)
+template <int G>
+__global__ void __launch_bounds__(DwShape<G>::kThreads, DwShape<G>::kCtas)
 ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
 {
-    constexpr int kWarps = DwShape<MT>::kWarps;
+    using Sh = DwShape<G>;
+    constexpr int kWarps = Sh::kWarps, kTok = Sh::kTok, kKeys = Sh::kKeys;
+    constexpr bool kLate = Sh::kLate;
     extern __shared__ __align__(1024) unsigned char dw_sm[];
     unsigned char *sm = dw_sm;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + DwSmem::kBar);
@@ -740,7 +748,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         *s_alive = *s_done = 0;
     }
     if (warp == 0) {
-        tmem_alloc(tmem_slot, kDwTmemCols);
+        tmem_alloc(tmem_slot, Sh::kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -811,6 +819,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             for (int c = 0; c < nc; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
+                const uint32_t d1 = tmem + kDwD1 + (c & 1) * Sh::kD1Step;
                 const uint32_t kb = s_base + DwSmem::kK + st * 16384, bb = s_base + DwSmem::kB + st * kDcHead;
                 // KH^T once the tile has landed and H(c) is written
                 if (!mbar_wait(bar_k + st, ph2, status) || !mbar_wait(arr_h, ph, status)) {
@@ -826,17 +835,17 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
                 for (int ks = 0; ks < a.nks; ++ks) {
                     const uint64_t kd = sw128_desc(kb + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024);
-                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, kd, kIdTok, ks > 0);
-                    umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks + 8, kd, kIdTok, 1);
+                    umma_bf16_ts(d1, tmem + kDwH + 16 * ks, kd, kIdTok, ks > 0);
+                    umma_bf16_ts(d1, tmem + kDwH + 16 * ks + 8, kd, kIdTok, 1);
                 }
                 commit(bar_kh);
-                // the products of c - 1, the last readers of the other stage and of P, completed
-                // before H(c) was written
-                if (c > 0) {
-                    if (outs)
-                        load_p(c);
-                    if (c + 1 < nc)
-                        load_kb(c + 1);
+                // the product that reads P has completed
+                if (c > 0 && outs) {
+                    if (!mbar_wait(bar_y, ph ^ 1, status)) {
+                        ok = false;
+                        break;
+                    }
+                    load_p(c);
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
                 if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
@@ -844,11 +853,15 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     break;
                 }
                 tc_fence_after();
+                // the other stage: dH(c - 1) has completed (before H(c) was written) and the
+                // outputs of c - 1 have left (before R(c) was written)
+                if (c > 0 && c + 1 < nc)
+                    load_kb(c + 1);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                     for (int ks = 0; ks < 2 + 2 * hf; ++ks) {
-                        const uint32_t dst = tmem + kDwD2 + 32 * hf, rhi = tmem + kDwD1 + 16 * ks, rlo = rhi + 8;
+                        const uint32_t dst = tmem + kDwD2 + 32 * hf, rhi = d1 + 16 * ks, rlo = rhi + 8;
                         const uint32_t to = bb + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0);
                         const uint64_t thi = sw32_desc(to + kDcThi), tlo = sw32_desc(to + kDcTlo);
                         umma_bf16_ts(dst, rhi, thi, kIdHalf, ks > 0);
@@ -869,9 +882,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     tc_fence_after();
                     for (int ks = 0; ks < a.nks; ++ks) {
                         const uint32_t qo = s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32;
-                        umma_bf16_ts(tmem + kDwD1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
-                        umma_bf16_ts(tmem + kDwD1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf,
-                                     ks > 0);
+                        umma_bf16_ts(d1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
+                        umma_bf16_ts(d1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf, ks > 0);
                     }
                     commit(bar_qh);
                 }
@@ -891,7 +903,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                         for (int ks = 0; ks < 2 + 2 * hf; ++ks)
-                            umma_bf16_ts(tmem + kDwD1 + 32 * hf, tmem + kDwU + 16 * ks,
+                            umma_bf16_ts(d1 + 32 * hf, tmem + kDwU + 16 * ks,
                                          sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)),
                                          kIdHalf, 1);
                     commit(bar_y);
@@ -933,16 +945,14 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
         }
     } else if (ok) {
         // ======================= the compute warps =======================================
-        // warp w: MT tiles m of 16 tensor-memory lanes from row0 (a warp reaches the lanes
-        // 32 (w % 4) .. + 31), half cg of the columns (keys 64 cg .. of H, tokens 32 cg .. of
-        // the chunk)
-        const int q4 = warp & 3, cg = (warp >> 2) & 1;
-        const int row0 = 32 * q4 + (MT == 1 ? 16 * (warp >> 3) : 0);
+        // warp w: two tiles m of 16 tensor-memory lanes from row0, group cg of the columns (keys
+        // kKeys cg .. of H, tokens kTok cg .. of the chunk)
+        const int row0 = 32 * (warp & 3), cg = warp >> 2;
         const int tr = lane >> 2, tc = 2 * (lane & 3); // this thread's row and column pair of a fragment
         const int col = n0 + row0 + tr;             // its first value column; the others 8 apart
         const uint32_t lanes = tmem + (uint32_t(row0) << 16);
-        // H[m][k][x]: value column col + 16 m + 8 x, keys 64 cg + 8 k + tc, + 1
-        float2 H[MT][8][2];
+        // H[m][k][x]: value column col + 16 m + 8 x, keys kKeys cg + 8 k + tc, + 1
+        float2 H[2][kKeys / 8][2];
         bool zero = false; // M has become 0
         // the state the segment starts from: h0, the state after the segment before it, the
         // identity, or zero
@@ -951,14 +961,14 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             from = a.seg_n + (bh * (a.segments - 1) + seg - 1) * a.dk * a.dv;
         else if (seg == 0 && a.h0 && !dc_cut(a.reset, a.g, b * a.seq, a.heads_v, h))
             from = (a.pass == 2 && a.seg_h0 ? a.seg_h0 : a.h0) + bh * a.dk * a.dv;
-        const int64_t sofs = int64_t(64 * cg + tc) * cols + col;
+        const int64_t sofs = int64_t(kKeys * cg + tc) * cols + col;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < kKeys / 8; ++k)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int key = 64 * cg + 8 * k + tc, vc = col + 16 * m + 8 * x;
+                    const int key = kKeys * cg + 8 * k + tc, vc = col + 16 * m + 8 * x;
                     const bool in = from && key < a.dk && vc < cols; // (dk is even)
                     const int64_t o = sofs + int64_t(8 * k) * cols + 16 * m + 8 * x;
                     H[m][k][x] = make_float2(in ? from[o] : 0.0f, in ? from[o + cols] : 0.0f);
@@ -977,7 +987,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     dw_split2(H[m][kb + i][x], w[2 * i + x], w[4 + 2 * i + x]);
-            tmem_st_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 8 * kb, w);
+            tmem_st_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + kKeys * cg + 8 * kb, w);
         };
         auto arrive = [&](uint64_t *bar) {
             tc_fence_before();
@@ -991,25 +1001,25 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             return good;
         };
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int kb = 0; kb < 8; kb += 2)
+            for (int kb = 0; kb < kKeys / 8; kb += 2)
                 store_h(m, kb);
         tmem_st_wait();
         arrive(arr_h);
-        const uint32_t v_base = s_base + DwSmem::kV + (q4 >> 1) * 8192; // the tile of this warp's values
-        unsigned char *ytile = sm + DwSmem::kY + warp * (1024 * MT);
+        const uint32_t v_base = s_base + DwSmem::kV + (row0 >> 6) * 8192; // the tile of this warp's values
+        unsigned char *ytile = sm + DwSmem::kY + warp * (64 * kTok);
         const uint32_t y_base = smem_u32(ytile);
-        // this lane's 16 bytes of the tile's first rows; rows 32 >> MT further on, ystep more
-        const int64_t ystep = int64_t(32 >> MT) * a.heads_v * a.dv;
-        __nv_bfloat16 *yp = a.y + ((b * a.seq + cb * kDcChunk + 32 * cg + (lane >> MT)) * a.heads_v + h) * a.dv + n0 + row0 +
-                            8 * (lane & (2 * MT - 1));
+        // this lane's 16 bytes of the tile's first eight rows; eight rows further on, ystep more
+        const int64_t ystep = int64_t(8) * a.heads_v * a.dv;
+        __nv_bfloat16 *yp = a.y + ((b * a.seq + cb * kDcChunk + kTok * cg + (lane >> 2)) * a.heads_v + h) * a.dv + n0 + row0 +
+                            8 * (lane & 3);
         for (int c = 0; c < nc; ++c) {
             const int st = c & 1;
             const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
             const unsigned char *blk = sm + DwSmem::kB + st * kDcHead;
-            const float *sc = reinterpret_cast<const float *>(blk + kDcC) + 32 * cg + tc;
-            const float *sw = reinterpret_cast<const float *>(blk + kDcW) + 32 * cg + tc;
+            const float *sc = reinterpret_cast<const float *>(blk + kDcC) + kTok * cg + tc;
+            const float *sw = reinterpret_cast<const float *>(blk + kDcW) + kTok * cg + tc;
             const float *ss_ = reinterpret_cast<const float *>(blk + kDcS);
             // the shared-memory addresses of a step are computed when it runs: kept over the
             // loop they would cost the registers that H needs
@@ -1052,14 +1062,14 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg;
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + (c & 1) * Sh::kD1Step + kTok * cg;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) { // 16 tokens
+                for (int j = 0; j < kTok / 16; ++j) { // 16 tokens
                     uint32_t r[8], v[4] = {}, w[8];
                     // 8 values x 8 tokens a matrix: x = matrix % 2, token block 2 j + matrix / 2
                     if (!for_m)
-                        ldmatrix_x4_trans(v, v_base + sw128_off(32 * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
+                        ldmatrix_x4_trans(v, v_base + sw128_off(kTok * cg + 16 * j + 8 * (ln >> 4) + (ln & 7),
                                                                 ((row0 & 63) >> 3) + 2 * m + ((ln >> 3) & 1)));
                     tmem_ld_frag(at + 16 * j, r);
 #pragma unroll
@@ -1085,10 +1095,10 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 break;
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + 32 * cg;
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + kTok * cg;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < kTok / 16; ++j) {
                     uint32_t r[8], w[8], u[4];
                     tmem_ld_frag(at + 16 * j, r);
 #pragma unroll
@@ -1102,27 +1112,25 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                         }
                     }
                     if (outs)
-                        tmem_st_frag(ml + kDwU + 16 * (2 * cg + j), u);
+                        tmem_st_frag(ml + kDwU + 16 * (kTok / 16 * cg + j), u);
                     tmem_st_frag(at + 16 * j, w);
                 }
             }
             tmem_st_wait();
             arrive(arr_u);
-            // ---- while dH^T runs: the outputs ---------------------------------------------
-            if (outs) {
-                if (!wait(bar_y, ph)) {
-                    ok = false;
-                    break;
-                }
+            // ---- the outputs: while dH^T runs, or once the state is handed on -----------------
+            auto emit = [&]() {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int m = 0; m < 2; ++m) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < kTok / 16; ++j) {
                         uint32_t r[8], o[4];
-                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 + 32 * cg + 16 * j, r);
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 +
+                                     (c & 1) * Sh::kD1Step + kTok * cg + 16 * j,
+                                 r);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + 32 * cg + 16 * j + 8 * i + tc);
+                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + kTok * cg + 16 * j + 8 * i + tc);
                             sv.x = em.y == 0.0f ? sv.x : 1.0f;
                             sv.y = em.y == 0.0f ? sv.y : 1.0f;
 #pragma unroll
@@ -1131,40 +1139,46 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                                 o[2 * i + x] = pack_bf16x2(y.x, y.y);
                             }
                         }
-                        // rows of 32 MT bytes (16 MT values) in the swizzle of that span: token 8 (2 j +
-                        // matrix / 2) + lane % 8, values 16 m + 8 (matrix % 2) ..
+                        // rows of 64 bytes in the 64-byte swizzle: token 8 (2 j + matrix / 2) + lane % 8,
+                        // values 16 m + 8 (matrix % 2) ..
                         const int t = 16 * j + 8 * (ln >> 4) + (ln & 7), ch = 2 * m + ((ln >> 3) & 1);
-                        stmatrix_x4_trans(y_base + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1)), o);
+                        stmatrix_x4_trans(y_base + 64 * t + 16 * (ch ^ ((t >> 1) & 3)), o);
                     }
                 }
                 __syncwarp();
                 // back as rows of the tile, 16 bytes a lane (a TMA store per warp and the proxy fence
                 // before it took three times as long)
                 {
-                    const int t = ln >> MT, ch = ln & (2 * MT - 1); // (the swizzle repeats every 8 rows)
-                    const unsigned char *src = ytile + 32 * MT * t + 16 * (ch ^ (MT == 2 ? (t >> 1) & 3 : (t >> 2) & 1));
-                    const int left = a.seq - (cb + c) * kDcChunk - 32 * cg - t;
+                    const int t = ln >> 2, ch = ln & 3; // (the swizzle repeats every 8 rows)
+                    const unsigned char *src = ytile + 64 * t + 16 * (ch ^ ((t >> 1) & 3));
+                    const int left = a.seq - (cb + c) * kDcChunk - kTok * cg - t;
                     const bool in = n0 + row0 + 8 * ch < a.dv; // (dv is a multiple of 8)
 #pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i)
-                        if (in && left > (32 >> MT) * i)
-                            *reinterpret_cast<uint4 *>(yp + i * ystep) =
-                                *reinterpret_cast<const uint4 *>(src + 32 * MT * (32 >> MT) * i);
-                    yp += (2 << MT) * ystep;
+                    for (int i = 0; i < kTok / 8; ++i)
+                        if (in && left > 8 * i)
+                            *reinterpret_cast<uint4 *>(yp + i * ystep) = *reinterpret_cast<const uint4 *>(src + 512 * i);
+                    yp += (kDcChunk / 8) * ystep;
                 }
+            };
+            if (outs && !kLate) {
+                if (!wait(bar_y, ph)) {
+                    ok = false;
+                    break;
+                }
+                emit();
             }
             // ---- H = E_63 H + dH -------------------------------------------------------------
-            if (!wait(bar_dh + cg, ph)) {
+            if (!wait(bar_dh + (kKeys * cg) / 64, ph)) {
                 ok = false;
                 break;
             }
 #pragma unroll
-            for (int kb = 0; kb < 8; kb += 2) { // 16 keys
-                if (4 * cg + kb / 2 < a.nks) {
+            for (int kb = 0; kb < kKeys / 8; kb += 2) { // 16 keys
+                if (kKeys / 16 * cg + kb / 2 < a.nks) {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
+                    for (int m = 0; m < 2; ++m) {
                         uint32_t r[8];
-                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + 64 * cg + 8 * kb, r);
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwH + kKeys * cg + 8 * kb, r);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -1178,9 +1192,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             if (for_m) {
                 bool any = false;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < kKeys / 8; ++k)
                         any = any || H[m][k][0].x != 0.0f || H[m][k][0].y != 0.0f || H[m][k][1].x != 0.0f ||
                               H[m][k][1].y != 0.0f;
                 if (any) // (NaN counts)
@@ -1188,6 +1202,13 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             }
             tmem_st_wait();
             arrive(arr_h);
+            if (outs && kLate) {
+                if (!wait(bar_y, ph)) {
+                    ok = false;
+                    break;
+                }
+                emit();
+            }
         }
         if (for_m && ok && tid == 0)
             a.seg_zero[bh * (a.segments - 2) + seg - 1] = zero;
@@ -1203,12 +1224,12 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             to = a.final_state + bh * a.dk * a.dv;
         if (ok && to) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kKeys / 8; ++k)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (64 * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < cols) {
+                        if (kKeys * cg + 8 * k + tc < a.dk && col + 16 * m + 8 * x < cols) {
                             const int64_t o = sofs + int64_t(8 * k) * cols + 16 * m + 8 * x;
                             to[o] = H[m][k][x].x;
                             to[o + cols] = H[m][k][x].y;
@@ -1220,7 +1241,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     __syncthreads();
     tc_fence_after();
     if (warp == 0)
-        tmem_dealloc(tmem, kDwTmemCols);
+        tmem_dealloc(tmem, Sh::kCols);
 }
 
 // ---- the join ------------------------------------------------------------------------

@@ -70,8 +70,8 @@ def test_long_ragged(orc, dtype):
     _check(orc, make_delta_inputs(1, 2051, 1, 2, 128, 128, dtype, seed=3100, h0=True), "long")
 
 
-@pytest.mark.parametrize("shape", [(1, 1300, 1, 1, 128, 128), (1, 1024, 2, 4, 64, 256), (2, 2000, 1, 3, 40, 24),
-                                   (1, 833, 4, 32, 128, 128), (3, 1531, 4, 12, 96, 64)])
+@pytest.mark.parametrize("shape", [(1, 6000, 1, 1, 128, 128), (1, 3024, 2, 4, 64, 256), (2, 2400, 1, 3, 40, 24),
+                                   (1, 2305, 4, 32, 128, 128), (3, 2331, 4, 12, 96, 64)])
 @pytest.mark.parametrize("resets", [0, 150])
 def test_segments(orc, shape, resets):
     """Few heads and a long prompt: the sequence is cut and walked in two passes.  With
@@ -322,7 +322,7 @@ def test_layer_prompt_decode_norm(orc, dtype):
     assert_close(o.cpu(), orc.group_norm(y.cpu(), 4, w, gate=z, center=False, eps=1e-6), TOL[o.dtype], "norm")
 
 
-@pytest.mark.parametrize("shape", [(2, 300, 1, 2, 128, 128), (1, 1600, 1, 2, 128, 128)])
+@pytest.mark.parametrize("shape", [(2, 300, 1, 2, 128, 128), (1, 2400, 1, 2, 128, 128)])
 def test_timed_out_waits_report_and_recover(shape):
     """Failure detection without a GPU fault: with an arrival of the first chunk withheld
     and the wait limit cut to 2 ms, the walk's waits give up, the status word reports
