@@ -550,9 +550,10 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
 // ---- the walk ------------------------------------------------------------------------
 
 // G: groups of four compute warps, each with a G-th of the columns: 2 (two CTAs per SM) or
-// 4 (one CTA per SM).  A CTA alone on its SM keeps Y^T of one chunk beside KH^T of the next
-// (D1 alternates between two places), so that the outputs leave after the state is handed
-// on, while the next chunk's first product runs.
+// 4 (one CTA per SM).  A CTA alone on its SM has room for Y^T beside the rest, in two places
+// that alternate: H^T Q^T follows KH^T at once, U^T P^T follows dH^T, and the outputs leave
+// after the state is handed on, while the next chunk's first product runs.  With two CTAs
+// Y^T takes R^T's place, between U^T and dH^T.
 template <int G> struct DwShape {
     static constexpr int kWarps = 4 * G;              // compute warps
     static constexpr int kThreads = 32 * kWarps + 32; // + the issuer warp
@@ -560,14 +561,16 @@ template <int G> struct DwShape {
     static constexpr int kTok = kDcChunk / G, kKeys = 128 / G; // columns of a warp: tokens, keys
     static constexpr bool kLate = G == 4;
     static constexpr uint32_t kCols = kLate ? 512 : 256; // tensor memory
-    static constexpr uint32_t kD1Step = kLate ? 128 : 0; // from D1 of even chunks to D1 of odd ones
+    static constexpr uint32_t kY = kLate ? 256 : 128;    // Y^T
+    static constexpr uint32_t kYStep = kLate ? 64 : 0;   // from Y^T of even chunks to that of odd ones
+    static constexpr uint32_t kU = kLate ? 384 : 72;     // U^T rounded, for Y: 16 tokens 16 columns apart
 };
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
-// then R^T over it in the same form (16 columns per 16 tokens), then Y^T.  D2: U^T, then
-// (w o U)^T over it.  U: U^T rounded, for Y, in the places of remainders of H that KH^T has
-// read (8 columns per 16 tokens, 16 columns apart).
-constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192, kDwU = 72;
+// then R^T over it in the same form (16 columns per 16 tokens).  D2: U^T, then
+// (w o U)^T over it.  U^T rounded, for Y, lies in the places of remainders of H that KH^T has
+// read, or has its own where there is room.
+constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192;
 
 struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kK = 0;                // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
@@ -816,10 +819,28 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             }
             if (nc > 1)
                 load_kb(1);
+            // H^T Q^T into Y^T
+            auto mul_qh = [&](uint32_t dy) {
+                for (int ks = 0; ks < a.nks; ++ks)
+                    umma_bf16_ts(dy, tmem + kDwH + 16 * ks,
+                                 sw128_desc(s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), kIdTok,
+                                 ks > 0);
+                commit(bar_qh);
+            };
+            // + U^T P^T, in halves of another shape: after H^T Q^T has completed
+            auto mul_up = [&](uint32_t dy) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int ks = 0; ks < 2 + 2 * hf; ++ks)
+                        umma_bf16_ts(dy + 32 * hf, tmem + Sh::kU + 16 * ks,
+                                     sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
+                commit(bar_y);
+            };
             for (int c = 0; c < nc; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
-                const uint32_t d1 = tmem + kDwD1 + (c & 1) * Sh::kD1Step;
+                const uint32_t d1 = tmem + kDwD1, dy = tmem + Sh::kY + (c & 1) * Sh::kYStep;
                 const uint32_t kb = s_base + DwSmem::kK + st * 16384, bb = s_base + DwSmem::kB + st * kDcHead;
                 // KH^T once the tile has landed and H(c) is written
                 if (!mbar_wait(bar_k + st, ph2, status) || !mbar_wait(arr_h, ph, status)) {
@@ -847,16 +868,20 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                     load_p(c);
                 }
+                if (outs && kLate) {
+                    if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mul_qh(dy);
+                }
                 // U^T once R is written: the blocks of T on and below the diagonal
                 if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // the other stage: dH(c - 1) has completed (before H(c) was written) and the
-                // outputs of c - 1 have left (before R(c) was written)
-                if (c > 0 && c + 1 < nc)
-                    load_kb(c + 1);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -870,49 +895,44 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                 }
                 commit(bar_u);
+                // the other stage: dH(c - 1) has completed (before H(c) was written) and the
+                // outputs of c - 1 have left (before R(c) was written)
+                if (c > 0 && c + 1 < nc)
+                    load_kb(c + 1);
                 if (c + 1 < nc && !for_m) // R(c), the only reader of v, is written
                     load_v(c + 1);
-                if (outs) {
-                    // Y^T over R: H^T Q^T, once R has been read
+                if (outs && kLate) {
+                    if (!mbar_wait(bar_qh, ph, status)) { // (long done)
+                        ok = false;
+                        break;
+                    }
+                    if (c + 1 < nc)
+                        load_q(c + 1);
+                }
+                if (outs && !kLate) { // Y^T over R, once R has been read
                     if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status) ||
                         !mbar_wait(bar_u, ph, status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int ks = 0; ks < a.nks; ++ks) {
-                        const uint32_t qo = s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32;
-                        umma_bf16_ts(d1, tmem + kDwH + 16 * ks, sw128_desc(qo, 16, 1024), kIdHalf, ks > 0);
-                        umma_bf16_ts(d1 + 32, tmem + kDwH + 16 * ks, sw128_desc(qo + 4096, 16, 1024), kIdHalf, ks > 0);
-                    }
-                    commit(bar_qh);
+                    mul_qh(dy);
                 }
-                // + U^T P^T, and dH^T over H, once U is written and H has been read: its first
-                // half while U^T P^T completes, whose U lies in the place of the second
-                if (!mbar_wait(arr_u, ph, status)) {
+                // U is written: dH^T over H, which has been read (with two CTAs its first half
+                // while U^T P^T completes, whose U lies in the place of the second)
+                if (!mbar_wait(arr_u, ph, status) || (outs && !mbar_wait(bar_p, ph, status))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (outs) {
-                    if (!mbar_wait(bar_p, ph, status)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                        for (int ks = 0; ks < 2 + 2 * hf; ++ks)
-                            umma_bf16_ts(d1 + 32 * hf, tmem + kDwU + 16 * ks,
-                                         sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)),
-                                         kIdHalf, 1);
-                    commit(bar_y);
+                if (outs && !kLate) {
                     if (!mbar_wait(bar_qh, ph, status)) {
                         ok = false;
                         break;
                     }
+                    tc_fence_after();
+                    mul_up(dy);
                 }
-                tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t kd = sw128_desc(kb + ks * 2048, 8192, 1024); // keys x 16 tokens (MN-major)
@@ -921,7 +941,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 }
                 commit(bar_dh);
                 if (a.nks > 4) {
-                    if (outs && !mbar_wait(bar_y, ph, status)) {
+                    if (outs && !kLate && !mbar_wait(bar_y, ph, status)) {
                         ok = false;
                         break;
                     }
@@ -934,7 +954,9 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                 }
                 commit(bar_dh + 1);
-                if (c + 1 < nc && outs)
+                if (outs && kLate)
+                    mul_up(dy);
+                if (c + 1 < nc && outs && !kLate)
                     load_q(c + 1);
             }
             // let every load and product in flight finish before the tensor memory is freed:
@@ -1063,7 +1085,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + (c & 1) * Sh::kD1Step + kTok * cg;
+                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD1 + kTok * cg;
 #pragma unroll
                 for (int j = 0; j < kTok / 16; ++j) { // 16 tokens
                     uint32_t r[8], v[4] = {}, w[8];
@@ -1112,7 +1134,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                         }
                     }
                     if (outs)
-                        tmem_st_frag(ml + kDwU + 16 * (kTok / 16 * cg + j), u);
+                        tmem_st_frag(ml + Sh::kU + 16 * (kTok / 16 * cg + j), u);
                     tmem_st_frag(at + 16 * j, w);
                 }
             }
@@ -1125,9 +1147,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
 #pragma unroll
                     for (int j = 0; j < kTok / 16; ++j) {
                         uint32_t r[8], o[4];
-                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + kDwD1 +
-                                     (c & 1) * Sh::kD1Step + kTok * cg + 16 * j,
-                                 r);
+                        tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + Sh::kY + (c & 1) * Sh::kYStep + kTok * cg + 16 * j,
+                                     r);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float2 sv = *reinterpret_cast<const float2 *>(ss_ + kTok * cg + 16 * j + 8 * i + tc);
