@@ -241,8 +241,11 @@ template <typename T, int VEC, int NV, bool CTA> int launch_group_norm(const ss:
     const int64_t per_cta = CTA ? 1 : ss::kGnThreads >> a.team_log2;
     const int64_t blocks = (a.rows * a.groups + per_cta - 1) / per_cta;
     const int64_t most = int64_t(sms) * 16;
-    ss::ss_group_norm_kernel<T, VEC, NV, CTA>
-        <<<unsigned(blocks < most ? blocks : most), ss::kGnThreads, 0, s>>>(a);
+    const unsigned grid = unsigned(blocks < most ? blocks : most);
+    if (VEC > 1 && a.size == (CTA ? ss::kGnThreads : 1 << a.team_log2) * VEC * NV)
+        ss::ss_group_norm_kernel<T, VEC, NV, CTA, (VEC > 1)><<<grid, ss::kGnThreads, 0, s>>>(a);
+    else
+        ss::ss_group_norm_kernel<T, VEC, NV, CTA, false><<<grid, ss::kGnThreads, 0, s>>>(a);
     return launch_status();
 }
 

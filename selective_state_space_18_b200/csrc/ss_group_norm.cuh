@@ -127,7 +127,9 @@ __host__ __device__ constexpr int gn_min_ctas(int elements)
 // One group per team and turn; teams take groups grid-strided.  A lane's elements are held
 // and worked on as pairs (packed fp32 arithmetic: two elements an instruction); the
 // instructions per element are what a group of many small rows is bound by.
-template <typename T, int VEC, int NV, bool CTA>
+// FULL: the group fills its team's vectors, so that nothing is guarded (with the guards
+// 16384 x 32 groups of 128 took 75 us, a third of their instructions being guards).
+template <typename T, int VEC, int NV, bool CTA, bool FULL>
 __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_norm_kernel(const GroupNormArgs a)
 {
     constexpr int kE = NV * VEC, kP = (kE + 1) / 2; // elements and pairs of a lane
@@ -144,20 +146,25 @@ __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_no
     int grp = int(item - row * a.groups);
     const bool gated = a.gate != nullptr, gate_first = gated && (a.mode & kGnGateFirst);
     const int c0 = VEC * lane; // this lane's first element; its vectors are VEC * team apart
+    auto in = [&](int i) { return FULL || c0 + VEC * team * i < a.size; }; // vector i is in the group
     // every lane of a warp makes the same number of turns (the sums are warp-collective)
     for (int64_t first = int64_t(blockIdx.x) * per_cta; first < total; first += step) {
-        const int size = item < total ? a.size : 0; // 0: nothing to do this turn
+        const bool live = item < total; // (teams past the end repeat the last group, unstored)
+        if (!live) {
+            row = a.rows - 1;
+            grp = a.groups - 1;
+        }
         const int64_t at = row * a.x_stride + int64_t(grp) * a.size;
         GnVec<T, VEC> xv[NV], zv[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (c0 + VEC * team * i < size)
+            if (in(i))
                 xv[i].load(static_cast<const T *>(a.x) + at + c0 + VEC * team * i);
         if (gated) {
             const int64_t zat = row * a.gate_stride + int64_t(grp) * a.size;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (c0 + VEC * team * i < size)
+                if (in(i))
                     zv[i].load(static_cast<const T *>(a.gate) + zat + c0 + VEC * team * i);
         }
         float2 x[kP];
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_no
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
                     v[e] = 0.0f;
-                if (c0 + VEC * team * i < size)
+                if (in(i))
                     raw[i].get(v);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_no
 #pragma unroll
             for (int e = 0; e < kE; ++e) { // (elements beyond the group stay 0)
                 float &f = e & 1 ? x[e / 2].y : x[e / 2].x;
-                f = c0 + VEC * team * (e / VEC) < size ? f - mean : 0.0f;
+                f = in(e / VEC) ? f - mean : 0.0f;
             }
         }
         float2 s2 = __fmul2_rn(x[0], x[0]);
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_no
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
                     v[e] = 0.0f;
-                if (c0 + VEC * team * i < size)
+                if (in(i))
                     gn_params<VEC>(src, pofs + VEC * team * i, v);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(kGnThreads, gn_min_ctas(NV * VEC)) ss_group_no
         T *yp = static_cast<T *>(a.y) + (row * a.groups + grp) * a.size + c0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (c0 + VEC * team * i < size) {
+            if (live && in(i)) {
                 float o[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
