@@ -407,7 +407,8 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *                 shapes that need none) the token-by-token kernel runs.
  *
  * heads_v must be a multiple of heads_k (SS_ERR_SHAPE), dk at most 256
- * (SS_ERR_UNSUPPORTED).  Inputs must be finite (but for g) where they are read.
+ * (SS_ERR_UNSUPPORTED).  An infinity or NaN among the inputs reaches the results that
+ * depend on it and no others: not earlier tokens, nor those behind a reset.
  *
  * Two forms:
  *  - bf16 with dk a multiple of 8 from 16 to 128, dv a multiple of 8, more than 16 tokens,
@@ -415,7 +416,8 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *    tokens on the tensor cores.  The state is held in float32 and its operands in 16 bits
  *    of mantissa (final_state follows float32 arithmetic to about 5e-6 of its size), the
  *    outputs' last products take bf16 operands.  Few heads and a long sequence are cut into
- *    segments that run at once;
+ *    segments that run at once.  Columns whose state becomes infinite or NaN are walked
+ *    once more token by token, about a microsecond each: right, but not fast;
  *  - every other case: token by token, all arithmetic in float32.
  * Results are the same from call to call.
  */

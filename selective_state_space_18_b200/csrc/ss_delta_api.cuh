@@ -155,6 +155,7 @@ int launch_delta_chunked(const ss::DeltaArgs &a, void *workspace, cudaStream_t s
     p.nchunks = int((a.seq + ss::kDcChunk - 1) / ss::kDcChunk);
     p.blocks = static_cast<unsigned char *>(workspace);
     ss::DeltaWalkArgs w{};
+    w.d = a;
     w.batch = a.batch;
     w.seq = int(a.seq);
     w.heads_v = a.heads_v;

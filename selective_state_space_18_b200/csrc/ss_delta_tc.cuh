@@ -589,6 +589,7 @@ struct DwSmem { // from a 1024-byte aligned base
 static_assert(DwSmem::kBytes <= 113 * 1024, "shared memory of the walk");
 
 struct DeltaWalkArgs {
+    DeltaArgs d; // as called: for the columns that are walked token by token
     int64_t batch;
     int seq, heads_v, ratio, dk, dv;
     int nchunks, col_tiles, nks;  // nks: 16-key slices of the state
@@ -696,9 +697,112 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t
                  : "memory");
 }
 
+// The columns n0 .. n0 + 127 of segment `seg` once more, token by token in fp32, where the
+// walk's state has become infinite or NaN.  In products over a chunk 0 times such a value
+// reaches tokens that do not depend on it (those before it, and those behind a reset); it
+// then always stays in the state, which the walk looks at once, at its end.  Here a token
+// only meets what it depends on.  From the state after the segment before when that is
+// finite, or from the first token.  Two syncs a token, two threads a column, the state in
+// shared memory: about a microsecond a token, for inputs that hold such values only.
+__device__ __noinline__ void delta_rewalk(const DeltaWalkArgs &a, unsigned char *sm, int64_t bh, int seg, int n0)
+{
+    const DeltaArgs &d = a.d;
+    float *st = reinterpret_cast<float *>(sm);              // [dk][128]
+    float *kq = st + 128 * 128;                             // two of k[128], q[128], (decay, beta, q . k)
+    float *part = kq + 2 * 264;                             // [2 halves][k . S, q . S][128]
+    const int tid = threadIdx.x, lane = tid & 31, col = tid & 127, half = tid >> 7;
+    const bool mine = tid < 256, in = n0 + col < a.dv;
+    const int64_t b = bh / a.heads_v;
+    const int h = int(bh % a.heads_v), hk = h / a.ratio;
+    const int k0 = half ? d.dk / 2 : 0, k1 = half ? d.dk : d.dk / 2; // this thread's keys
+    const int64_t ofs = bh * a.dk * a.dv + n0 + col;
+    auto load = [&](const float *from) {
+        bool bad = false;
+        for (int i = k0; mine && i < k1; ++i) {
+            const float x = from && in ? from[int64_t(i) * a.dv] : 0.0f;
+            bad = bad || !(fabsf(x) < INFINITY);
+            st[i * 128 + col] = x;
+        }
+        return __syncthreads_or(bad);
+    };
+    int64_t t = int64_t(seg) * a.seg_chunks * kDcChunk;
+    const int64_t first = t, last = t + int64_t(a.seg_chunks) * kDcChunk, end = last < a.seq ? last : a.seq;
+    const float *h0 = a.pass == 2 && a.seg_h0 ? a.seg_h0 : a.h0;
+    if (seg == 0 || load(a.seg_n + (bh * (a.segments - 1) + seg - 1) * a.dk * a.dv + n0 + col)) {
+        t = 0;
+        load(h0 ? h0 + ofs : nullptr);
+    }
+    for (; t < end; ++t) {
+        const int64_t tok = b * a.seq + t;
+        float *buf = kq + (t & 1) * 264;
+        if (tid < 32) {
+            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(d.q) + tok * d.q_stride + int64_t(hk) * d.dk;
+            const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(d.k) + tok * d.k_stride + int64_t(hk) * d.dk;
+            float q[4], k[4], qq = 0.0f, kk = 0.0f, qk = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = lane + 32 * j;
+                q[j] = i < d.dk ? __bfloat162float(qp[i]) : 0.0f;
+                k[j] = i < d.dk ? __bfloat162float(kp[i]) : 0.0f;
+                qq = fmaf(q[j], q[j], qq);
+                kk = fmaf(k[j], k[j], kk);
+                qk = fmaf(q[j], k[j], qk);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                qq += __shfl_xor_sync(0xffffffffu, qq, o);
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                qk += __shfl_xor_sync(0xffffffffu, qk, o);
+            }
+            const float rq = d.l2norm ? d.scale * rsqrtf(qq + kDeltaEps) : d.scale;
+            const float rk = d.l2norm ? rsqrtf(kk + kDeltaEps) : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                buf[lane + 32 * j] = rk * k[j];
+                buf[128 + lane + 32 * j] = rq * q[j];
+            }
+            if (lane == 0) {
+                const int64_t gi = tok * a.heads_v + h;
+                buf[256] = d.reset && d.reset[tok] ? 0.0f : d.g ? expf(d.g[gi]) : 1.0f;
+                buf[257] = d.beta ? d.beta[gi] : 1.0f;
+                buf[258] = qk * rq * rk;
+            }
+        }
+        __syncthreads();
+        const float decay = buf[256];
+        if (mine) {
+            float ks = 0.0f, qs = 0.0f;
+            if (decay != 0.0f) // a decay of 0 discards the state, whatever it holds
+                for (int i = k0; i < k1; ++i) {
+                    const float x = st[i * 128 + col];
+                    ks = fmaf(buf[i], x, ks);
+                    qs = fmaf(buf[128 + i], x, qs);
+                }
+            part[half * 256 + col] = ks;
+            part[half * 256 + 128 + col] = qs;
+        }
+        __syncthreads();
+        if (mine) {
+            const float ks = decay * (part[col] + part[256 + col]), qs = decay * (part[128 + col] + part[384 + col]);
+            const int64_t ch = int64_t(h) * a.dv + n0 + col;
+            const float v = in ? __bfloat162float(static_cast<const __nv_bfloat16 *>(d.v)[tok * d.v_stride + ch]) : 0.0f;
+            const float u = buf[257] * (v - ks);
+            for (int i = k0; i < k1; ++i) {
+                const float x = decay == 0.0f ? 0.0f : decay * st[i * 128 + col];
+                st[i * 128 + col] = fmaf(buf[i], u, x);
+            }
+            if (half == 0 && in && t >= first)
+                a.y[tok * a.heads_v * a.dv + ch] = __float2bfloat16_rn(fmaf(buf[258], u, qs));
+        }
+    }
+    if (a.final_state && seg == a.segments - 1)
+        for (int i = k0; mine && in && i < k1; ++i)
+            a.final_state[ofs + int64_t(i) * a.dv] = st[i * 128 + col];
+}
+
 template <int G>
 __global__ void __launch_bounds__(DwShape<G>::kThreads, DwShape<G>::kCtas)
-ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
+ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
 {
     using Sh = DwShape<G>;
     constexpr int kWarps = Sh::kWarps, kTok = Sh::kTok, kKeys = Sh::kKeys;
@@ -763,6 +867,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     if (!ok && tid == 0)
         atomicOr(status, 1u << kStatusTimeout);
 
+    int bad = 0; // the walk's state is not finite
     if (ok && issuer) {
         // ======================= the issuer warp (one thread works) =======================
         if (elect_one()) {
@@ -965,6 +1070,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                 if ((begun >> i) & 1u)
                     mbar_wait(bars + i, (latest >> i) & 1u, nullptr);
         }
+        __syncwarp();
+        bad = __syncthreads_or(0);
     } else if (ok) {
         // ======================= the compute warps =======================================
         // warp w: two tiles m of 16 tensor-memory lanes from row0, group cg of the columns (keys
@@ -1167,8 +1274,7 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
                     }
                 }
                 __syncwarp();
-                // back as rows of the tile, 16 bytes a lane (a TMA store per warp and the proxy fence
-                // before it took three times as long)
+                // back as rows of the tile, 16 bytes a lane
                 {
                     const int t = ln >> 2, ch = ln & 3; // (the swizzle repeats every 8 rows)
                     const unsigned char *src = ytile + 64 * t + 16 * (ch ^ ((t >> 1) & 3));
@@ -1243,7 +1349,20 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
             to = a.seg_n + (bh * (a.segments - 1) + seg) * a.dk * a.dv;
         else if (seg == a.segments - 1 && a.final_state)
             to = a.final_state + bh * a.dk * a.dv;
-        if (ok && to) {
+        if (outs && ok) { // (0 x is 0 for finite x alone)
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int k = 0; k < kKeys / 8; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        sum = __ffma2_rn(make_float2(0.0f, 0.0f), H[m][k][x], sum);
+            bad = sum.x != 0.0f || sum.y != 0.0f;
+        }
+        __syncwarp();
+        bad = __syncthreads_or(bad); // before h0's place may take the final state
+        if (ok && to && !(outs && bad)) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1263,6 +1382,8 @@ ss_delta_walk_kernel(const DeltaWalkArgs a, const __grid_constant__ DeltaWalkMap
     tc_fence_after();
     if (warp == 0)
         tmem_dealloc(tmem, Sh::kCols);
+    if (bad)
+        delta_rewalk(a, sm, bh, seg, n0);
 }
 
 // ---- the join ------------------------------------------------------------------------

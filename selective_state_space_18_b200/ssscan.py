@@ -774,7 +774,8 @@ def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None
     q, "final_state": [batch, heads_v, dk, dv] float32 (None when not returned)}.
 
     workspace: True (allocated for the call), False (none: the token-by-token kernel) or a
-    uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself."""
+    uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself.
+    An infinity or NaN reaches the results that depend on it and no others."""
     index, dt = q.get_device(), q.dtype
     if stream is not None or index < 0 or index != torch.cuda.current_device():
         return _elsewhere(ss_delta_scan, q, stream, k, v, g, beta, reset=reset, h0=h0, scale=scale,

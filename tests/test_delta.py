@@ -144,6 +144,56 @@ def test_reset_forgets_what_came_before():
     assert torch.equal(y[:, 128:], y3) and torch.equal(fs, fs3)
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "h0"])
+@pytest.mark.parametrize("seq,heads_v,dtype,workspace", [(250, 2, "bf16", True), (250, 150, "bf16", True), (2400, 2, "bf16", True),
+                                                         (250, 2, "f32", True), (250, 2, "bf16", False)])
+def test_values_that_are_not_finite_stay_where_they_belong(orc, seq, heads_v, dtype, workspace, where, value):
+    """An infinity or NaN in one token reaches neither earlier tokens nor those behind a
+    reset, wherever in a chunk both lie; one in h0 nothing behind the first reset.  In every
+    form: one walk, many, segments, token by token."""
+    if where == "g" and value == math.inf:
+        pytest.skip("log decays lie below infinity")
+    for at, cut in ((200, 201), (191, 192), (100, 180), (0, 70), (seq - 1, None)):
+        clean = make_delta_inputs(1, seq, 1, heads_v, 64, 136, dtype, seed=3125, h0=True)
+        clean["reset"] = torch.zeros(1, seq, dtype=torch.uint8)
+        if cut is not None:
+            clean["reset"][0, cut] = 1
+        inp = {k: v.clone() for k, v in clean.items()}
+        if where == "h0":
+            inp["h0"][0, heads_v - 1] = value
+        else:
+            inp[where][0, at, -1] = value
+        y, fs = _scan(inp, scale=1.0, qk_l2norm=True, workspace=workspace)
+        ref = orc.delta_scan(**clean, scale=1.0, qk_l2norm=True)
+        before = at if where != "h0" else 0
+        assert_close(y[:, :before], ref["outputs"][:, :before], TOL[y.dtype], f"before {at}")
+        if cut is not None:
+            assert_close(y[:, cut:], ref["outputs"][:, cut:], TOL[y.dtype], f"from the reset at {cut}")
+            assert_close(fs, ref["final_state"], TOL[F32], "final state")
+        elif where in "kv":
+            assert not torch.isfinite(y[:, at:]).all() or not torch.isfinite(fs).all()
+        if where in ("v", "h0", "g", "beta") and heads_v > 1:   # the other heads know nothing of it
+            assert_close(y[:, :, 0], ref["outputs"][:, :, 0], TOL[y.dtype], "another head")
+
+
+@pytest.mark.parametrize("seq", [250, 2400])
+def test_chaining_in_place_after_a_nan(orc, seq):
+    """The final state may take h0's place in columns that are walked token by token too."""
+    clean = make_delta_inputs(1, seq, 1, 2, 128, 128, "bf16", seed=3126, h0=True)
+    clean["reset"] = torch.zeros(1, seq, dtype=torch.uint8)
+    clean["reset"][0, 30] = 1
+    ref = orc.delta_scan(**clean, scale=1.0, qk_l2norm=True)
+    inp = _cuda_dict(clean)
+    inp["v"][0, 20, 1, 5] = math.nan
+    inp["h0"][0, 0] = math.nan
+    out = ssscan.ss_delta_scan(**inp, scale=1.0, qk_l2norm=True, final_state=inp["h0"])
+    assert ssscan.ss_debug_status() == "SS_OK"
+    assert_close(out["outputs"].cpu()[:, 30:], ref["outputs"][:, 30:], TOL[BF16], "outputs")
+    assert_close(out["outputs"].cpu()[:, :20, 1], ref["outputs"][:, :20, 1], TOL[BF16], "outputs before")
+    assert_close(inp["h0"].cpu(), ref["final_state"], TOL[F32], "final state in h0's place")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_slices_of_one_projection(orc, dtype):
     """q, k and v as views of one buffer, read in place, equal the packed copies; rows
