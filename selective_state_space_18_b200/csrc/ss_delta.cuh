@@ -31,183 +31,315 @@ struct DeltaArgs {
     int l2norm;
 };
 
-// ---- prompt scan, token by token -----------------------------------------------------
+// ---- prompt scan in fp32, four tokens a step -----------------------------------------
 //
-// A CTA owns one (batch row, value head) and 16 of its value columns: columns of the
-// state never meet.  Four consumer warps hold the state in registers, a column's dk rows
-// over 8 lanes; eight producer warps stage the next 16 tokens, two each (q and k in fp32,
-// normalised and scaled, zero-padded to the kernel's dk; v; the decay, beta and q . k),
-// while the consumers walk the current ones.  Per token a consumer lane reads its 4 R4 rows of k
-// and q with 16-byte loads (four columns of a warp share each), and the two dot products
-// are reduced over the 8 lanes together.  What bounds it is the latency of that chain,
-// token after token, so it serves fp32 storage, key sizes the chunked form does not take
-// and prompts of a few tokens; all its arithmetic is fp32.
+// A CTA owns one (batch row, value head) and 16 or 4 of its value columns: columns of the
+// state never meet.  Consumer warps hold the state in registers, a column's dk rows over 8
+// lanes; eight producer warps stage the next 32 tokens, a step of four each, while the
+// consumers walk the current ones, and read the tile after that into registers.
+//
+// What bounds it is the latency of the chain from one state to the next: dot products with
+// the state, their sum over the 8 lanes, the write.  So four tokens 0..3 are taken from one
+// state S: with a_i their decays, A_i = a_0 .. a_i and D_ij = a_{j+1} .. a_i,
+//   u_i = beta_i (v_i - A_i S^T k_i) - sum_{j<i} beta_i D_ij (k_i . k_j) u_j
+//   y_i = A_i S^T q_i + sum_{j<=i} D_ij (q_i . k_j) u_j
+//   S'  = A_3 S + sum_j D_3j k_j u_j^T
+// The factors between tokens come from the producers.  Sums over lanes are exchanges that
+// halve the number of values a lane holds: eight values over 8 lanes in 7 shuffles, a
+// step's 24 products of rows over a warp in 31.  A step with a decay of 0, or with a
+// product of decays past 1e30, is walked token by token: 0 times an infinity or NaN that a
+// reset discards, or an infinity times an empty state, would come out of the products.
+// All arithmetic is fp32.  It serves fp32 storage, sizes and strides that the tensor-core
+// form does not take, and prompts of a few tokens.
+//
+// Measured (fp32): 2 x 300 tokens x 4 heads of 64: 32.5 us, against 48.7 us one token a
+// step; 4 x 2000 tokens x 4 heads of 64: 202 us against 309 us; 300 tokens x 2 heads of 256:
+// 67 us against 86 us.  What has a few tokens only, or many heads on every SM, loses a
+// little (16 heads of 128 x 4 tokens 6.6 us against 4.7; 256 heads x 300 tokens 659 us
+// against 633).  Rows read a step ahead
+// into registers made it slower (57 us from 40 with keys of 128).
 
-constexpr int kDrCols = 16, kDrTok = 16, kDrConsumers = 128, kDrProducers = 256;
-constexpr int kDrThreads = kDrConsumers + kDrProducers;
+// CW: consumer warps.  They share the SM's path to shared memory, of which a 16-byte read
+// that four columns of a warp have in common takes four turns; where the grid is small, CTAs
+// of one warp each spread that over more SMs.
+constexpr int kDrTok = 32, kDrStep = 4, kDrProducers = 256;
+constexpr int dr_cols(int cw) { return 4 * cw; }
+constexpr int dr_threads(int cw) { return 32 * cw + kDrProducers; }
+static_assert(kDrProducers / 32 == kDrTok / kDrStep, "a producer warp a step");
 
-template <int R4> struct DeltaRecSmem { // floats of one staging buffer
+template <int R4, int CW> struct DeltaRecSmem { // floats of one staging buffer
     static constexpr int kDk = 32 * R4; // padded key size
-    static constexpr int kK = 0, kQ = kDrTok * kDk, kV = 2 * kDrTok * kDk, kS = kV + kDrTok * kDrCols;
-    static constexpr int kFloats = kS + 4 * kDrTok; // per token: decay, beta, q . k, (unused)
+    static constexpr int kVRow = kDrTok + 4;
+    static constexpr int kK = 0, kQ = kDrTok * kDk, kV = 2 * kDrTok * kDk /* [column][token] */, kS = kV + dr_cols(CW) * kVRow;
+    // factors of a step: A_i, beta_i, D_3j, a_i (4 each), beta_i D_ij k_i.k_j for ij = 10 20 21 30
+    // 31 32, whether it goes token by token, (unused), D_ij q_i.k_j as 4 x 4 rows
+    static constexpr int kA = 0, kBeta = 4, kD3 = 8, kDecay = 12, kC = 16, kSingle = 22, kE = 24, kStep = 40;
+    static constexpr int kFloats = kS + kStep * (kDrTok / kDrStep);
     static constexpr size_t kBytes = 2 * size_t(kFloats) * 4;
 };
 
-template <typename T, int R4>
-__global__ void __launch_bounds__(kDrThreads) ss_delta_rec_kernel(const DeltaArgs a)
+// Sums of N values over groups of N lanes: lane l of a group is left with that of value l.
+template <int N> __device__ __forceinline__ float dr_sums(float (&v)[N], int lane)
 {
-    using Sm = DeltaRecSmem<R4>;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+template <typename T, int R4, int CW>
+__global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const DeltaArgs a)
+{
+    using Sm = DeltaRecSmem<R4, CW>;
+    constexpr int kDrCols = dr_cols(CW), kDrConsumers = 32 * CW;
+    constexpr int kVs = (kDrStep * kDrCols + 31) / 32; // values of v a producer lane loads
     extern __shared__ __align__(16) float dr_sm[];
     const int tid = threadIdx.x, lane = tid & 31;
     const int tiles = (a.dv + kDrCols - 1) / kDrCols;
-    const int c0 = int(blockIdx.x % tiles) * kDrCols;
-    const int64_t bh = blockIdx.x / tiles;
+    const int c0 = int(blockIdx.x % unsigned(tiles)) * kDrCols;
+    const int64_t bh = blockIdx.x / unsigned(tiles);
     const int64_t b = bh / a.heads_v;
     const int h = int(bh % a.heads_v), hk = h / a.ratio;
     const int64_t tok0 = b * a.seq; // first token of this batch row
     const int64_t ntiles = (a.seq + kDrTok - 1) / kDrTok;
 
-    // producer warp w stages tokens w and w + 8 of a tile, the loads of both in flight together
-    auto stage = [&](int64_t tile, float *buf) {
-        constexpr int kPer = kDrTok / (kDrProducers / 32);
+    if (tid >= kDrConsumers) {
+        // ======================= producers: warp w has step w of every tile ================
         const int w = (tid - kDrConsumers) >> 5;
-        float q[kPer][R4], k[kPer][R4], v[kPer], g[kPer], be[kPer];
+        float k[4][R4], q[4][R4], v[kVs], g, be;
+        // Tokens past the end are staged as k = q = v = 0, beta = 0, no decay: they change nothing.
+        auto fetch = [&](int64_t tile) {
+            const int64_t pos0 = tile * kDrTok + kDrStep * w;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int64_t pos = tile * kDrTok + w + u * (kDrProducers / 32);
-            const bool in = pos < a.seq;
-            const int64_t tok = tok0 + (in ? pos : 0), gi = tok * a.heads_v + h;
-            const T *qp = static_cast<const T *>(a.q) + tok * a.q_stride + int64_t(hk) * a.dk;
-            const T *kp = static_cast<const T *>(a.k) + tok * a.k_stride + int64_t(hk) * a.dk;
-            const T *vp = static_cast<const T *>(a.v) + tok * a.v_stride + int64_t(h) * a.dv + c0;
+            for (int u = 0; u < 4; ++u) {
+                const bool in = pos0 + u < a.seq;
+                const int64_t tok = tok0 + (in ? pos0 + u : 0);
+                const T *qp = static_cast<const T *>(a.q) + tok * a.q_stride + int64_t(hk) * a.dk;
+                const T *kp = static_cast<const T *>(a.k) + tok * a.k_stride + int64_t(hk) * a.dk;
 #pragma unroll
-            for (int j = 0; j < R4; ++j) {
-                const int i = lane + 32 * j;
-                q[u][j] = in && i < a.dk ? Elem<T>::load(qp + i) : 0.0f;
-                k[u][j] = in && i < a.dk ? Elem<T>::load(kp + i) : 0.0f;
+                for (int j = 0; j < R4; ++j) {
+                    const int i = lane + 32 * j;
+                    k[u][j] = in && i < a.dk ? Elem<T>::load(kp + i) : 0.0f;
+                    q[u][j] = in && i < a.dk ? Elem<T>::load(qp + i) : 0.0f;
+                }
             }
-            v[u] = in && lane < kDrCols && c0 + lane < a.dv ? Elem<T>::load(vp + lane) : 0.0f;
-            g[u] = a.g ? __ldg(a.g + gi) : 0.0f;
-            be[u] = a.beta ? __ldg(a.beta + gi) : 1.0f;
-            if (a.reset && a.reset[tok])
-                g[u] = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kVs; ++u) { // 4 tokens x kDrCols columns
+                const int64_t pos = pos0 + (32 * u + lane) / kDrCols;
+                const int c = c0 + lane % kDrCols;
+                v[u] = 32 * u + lane < kDrStep * kDrCols && pos < a.seq && c < a.dv
+                           ? Elem<T>::load(static_cast<const T *>(a.v) + (tok0 + pos) * a.v_stride + int64_t(h) * a.dv + c)
+                           : 0.0f;
+            }
+            g = 0.0f, be = 0.0f; // lane u < 4: of token u
+            if (lane < 4 && pos0 + lane < a.seq) {
+                const int64_t tok = tok0 + pos0 + lane, gi = tok * a.heads_v + h;
+                g = a.g ? __ldg(a.g + gi) : 0.0f;
+                be = a.beta ? __ldg(a.beta + gi) : 1.0f;
+                if (a.reset && a.reset[tok])
+                    g = -INFINITY;
+            }
+        };
+        auto stage = [&](float *buf) {
+            float *f = buf + Sm::kS + Sm::kStep * w;
+            // value 4 i + j (j <= i): q_i . k_j; 16 + 4 i + j: k_i . k_j; 17, 18, 19, 22: |q_i|^2
+            float s[32] = {};
+#pragma unroll
+            for (int x = 0; x < R4; ++x) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) {
+                        s[4 * i + j] = fmaf(q[i][x], k[j][x], s[4 * i + j]);
+                        s[16 + 4 * i + j] = fmaf(k[i][x], k[j][x], s[16 + 4 * i + j]);
+                    }
+                    const int qi = i < 3 ? 17 + i : 22;
+                    s[qi] = fmaf(q[i][x], q[i][x], s[qi]);
+                }
+            }
+            const float sum = dr_sums<32>(s, lane);
+            const float r = a.l2norm ? rsqrtf(sum + kDeltaEps) : 1.0f;
+            float rk[4], rq[4], dec[4], beta[4];
+            const float e = expf(g);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                rk[u] = __shfl_sync(0xffffffffu, r, 16 + 5 * u);
+                rq[u] = a.scale * __shfl_sync(0xffffffffu, r, u < 3 ? 17 + u : 22);
+                dec[u] = __shfl_sync(0xffffffffu, e, u);
+                beta[u] = __shfl_sync(0xffffffffu, be, u);
+#pragma unroll
+                for (int j = 0; j < R4; ++j) {
+                    buf[Sm::kK + (kDrStep * w + u) * Sm::kDk + lane + 32 * j] = rk[u] * k[u][j];
+                    buf[Sm::kQ + (kDrStep * w + u) * Sm::kDk + lane + 32 * j] = rq[u] * q[u][j];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kVs; ++u)
+                if (32 * u + lane < kDrStep * kDrCols)
+                    buf[Sm::kV + lane % kDrCols * Sm::kVRow + kDrStep * w + (32 * u + lane) / kDrCols] = v[u];
+            // this lane's product: factors picked by its i and j
+            const int i = (lane >> 2) & 3, j = lane & 3;
+            auto pick = [](const float (&x)[4], int n) { return n < 2 ? (n ? x[1] : x[0]) : (n == 2 ? x[2] : x[3]); };
+            const float d = (j < 1 && i >= 1 ? dec[1] : 1.0f) * (j < 2 && i >= 2 ? dec[2] : 1.0f) * (j < 3 && i >= 3 ? dec[3] : 1.0f);
+            const float dk = d * (sum * pick(rk, j));
+            if (lane < 16)
+                f[Sm::kE + lane] = j <= i ? dk * pick(rq, i) : 0.0f;
+            else if (j < i)
+                f[Sm::kC + i * (i - 1) / 2 + j] = pick(beta, i) * (dk * pick(rk, i));
+            const float a01 = dec[0] * dec[1], a12 = dec[1] * dec[2], a23 = dec[2] * dec[3];
+            if (lane == 0) {
+                const float4 A = make_float4(dec[0], a01, a01 * dec[2], a01 * a23);
+                const float4 D = make_float4(a12 * dec[3], a23, dec[3], 1.0f);
+                *reinterpret_cast<float4 *>(f + Sm::kA) = A;
+                *reinterpret_cast<float4 *>(f + Sm::kBeta) = make_float4(beta[0], beta[1], beta[2], beta[3]);
+                *reinterpret_cast<float4 *>(f + Sm::kD3) = D;
+                *reinterpret_cast<float4 *>(f + Sm::kDecay) = make_float4(dec[0], dec[1], dec[2], dec[3]);
+                const float most = fmaxf(fmaxf(fmaxf(A.x, A.y), fmaxf(A.z, A.w)),
+                                         fmaxf(fmaxf(fmaxf(D.x, D.y), fmaxf(D.z, a12)), fmaxf(dec[1], dec[2])));
+                const bool zero = dec[0] == 0.0f || dec[1] == 0.0f || dec[2] == 0.0f || dec[3] == 0.0f;
+                f[Sm::kSingle] = zero || most > 1e30f ? 1.0f : 0.0f;
+            }
+        };
+        fetch(0);
+        stage(dr_sm);
+        __syncthreads();
+        if (ntiles > 1)
+            fetch(1);
+        for (int64_t tile = 0; tile < ntiles; ++tile) {
+            if (tile + 1 < ntiles) {
+                stage(dr_sm + int((tile + 1) & 1) * Sm::kFloats);
+                if (tile + 2 < ntiles)
+                    fetch(tile + 2);
+            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int t = w + u * (kDrProducers / 32);
-            float qq = 0.0f, kk = 0.0f, qk = 0.0f;
-#pragma unroll
-            for (int j = 0; j < R4; ++j) {
-                qq = fmaf(q[u][j], q[u][j], qq);
-                kk = fmaf(k[u][j], k[u][j], kk);
-                qk = fmaf(q[u][j], k[u][j], qk);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                qq += __shfl_xor_sync(0xffffffffu, qq, o);
-                kk += __shfl_xor_sync(0xffffffffu, kk, o);
-                qk += __shfl_xor_sync(0xffffffffu, qk, o);
-            }
-            float rq = a.scale, rk = 1.0f;
-            if (a.l2norm) {
-                rq *= rsqrtf(qq + kDeltaEps);
-                rk = rsqrtf(kk + kDeltaEps);
-            }
-#pragma unroll
-            for (int j = 0; j < R4; ++j) {
-                buf[Sm::kQ + t * Sm::kDk + lane + 32 * j] = rq * q[u][j];
-                buf[Sm::kK + t * Sm::kDk + lane + 32 * j] = rk * k[u][j];
-            }
-            if (lane < kDrCols)
-                buf[Sm::kV + t * kDrCols + lane] = v[u];
-            if (lane == 0)
-                *reinterpret_cast<float4 *>(buf + Sm::kS + 4 * t) = make_float4(expf(g[u]), be[u], qk * rq * rk, 0.0f);
-        }
-    };
-
-    const bool consumer = tid < kDrConsumers;
-    const int col = tid >> 3, p = tid & 7; // consumer: its column, its lane of 8
-    const bool live = consumer && c0 + col < a.dv;
-    float S[4 * R4];
-#pragma unroll
-    for (int i = 0; i < 4 * R4; ++i)
-        S[i] = 0.0f;
-    const int64_t sbase = bh * a.dk * a.dv + c0 + col;
-    if (live && a.h0) {
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) {
-            const int row = 4 * (p + 8 * (i >> 2)) + (i & 3);
-            if (row < a.dk)
-                S[i] = a.h0[sbase + int64_t(row) * a.dv];
-        }
+        return;
     }
-    if (!consumer)
-        stage(0, dr_sm);
+
+    // ======================= consumers: eight lanes a column ===============================
+    const int col = tid >> 3, p = tid & 7;
+    const bool live = c0 + col < a.dv;
+    float2 S[2 * R4]; // rows 4 (p + 8 j) .. + 3
+    const int64_t sbase = bh * a.dk * a.dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < 2 * R4; ++i) {
+        const int row = 4 * (p + 8 * (i >> 1)) + 2 * (i & 1);
+        const bool in = live && a.h0;
+        S[i].x = in && row < a.dk ? a.h0[sbase + int64_t(row) * a.dv] : 0.0f;
+        S[i].y = in && row + 1 < a.dk ? a.h0[sbase + int64_t(row + 1) * a.dv] : 0.0f;
+    }
     __syncthreads();
-    T *yp = static_cast<T *>(a.y) + (tok0 * a.heads_v + h) * a.dv + c0 + col;
     const int64_t ystep = int64_t(a.heads_v) * a.dv;
+    const int yi = p & 3; // lane 4 + i of a column writes the output of token i of a step
+    T *yp = static_cast<T *>(a.y) + ((tok0 + yi) * a.heads_v + h) * a.dv + c0 + col;
     for (int64_t tile = 0; tile < ntiles; ++tile) {
-        if (!consumer) {
-            if (tile + 1 < ntiles)
-                stage(tile + 1, dr_sm + int((tile + 1) & 1) * Sm::kFloats);
-        } else {
-            const float *buf = dr_sm + int(tile & 1) * Sm::kFloats;
-            const int64_t left = a.seq - tile * kDrTok;
-            const int n = left < kDrTok ? int(left) : kDrTok;
-            for (int t = 0; t < n; ++t) {
-                const float4 *k4 = reinterpret_cast<const float4 *>(buf + Sm::kK + t * Sm::kDk) + p;
-                const float4 *q4 = reinterpret_cast<const float4 *>(buf + Sm::kQ + t * Sm::kDk) + p;
-                const float4 sc = *reinterpret_cast<const float4 *>(buf + Sm::kS + 4 * t);
-                const float v = buf[Sm::kV + t * kDrCols + col];
-                if (sc.x == 0.0f) { // a decay of 0 discards the state, whatever it holds
+        const float *buf = dr_sm + int(tile & 1) * Sm::kFloats;
+        const int64_t left = a.seq - tile * kDrTok;
+        const int n = left < kDrTok ? int(left) : kDrTok;
+#pragma unroll 1
+        for (int t = 0; t < n; t += kDrStep, yp += kDrStep * ystep) {
+            const float4 *k4 = reinterpret_cast<const float4 *>(buf + Sm::kK + t * Sm::kDk) + p;
+            const float4 *q4 = reinterpret_cast<const float4 *>(buf + Sm::kQ + t * Sm::kDk) + p;
+            const float *f = buf + Sm::kS + Sm::kStep * (t / kDrStep), *vp = buf + Sm::kV + col * Sm::kVRow + t;
+            if (f[Sm::kSingle] != 0.0f) { // token by token
+#pragma unroll 1
+                for (int u = 0; u < 4; ++u) {
+                    const float d = f[Sm::kDecay + u];
+                    float2 ks2 = make_float2(0.0f, 0.0f), qs2 = ks2;
 #pragma unroll
-                    for (int i = 0; i < 4 * R4; ++i)
-                        S[i] = 0.0f;
+                    for (int i = 0; i < 2 * R4; ++i) // a decay of 0 discards the state, whatever it holds
+                        S[i] = d == 0.0f ? make_float2(0.0f, 0.0f) : __fmul2_rn(make_float2(d, d), S[i]);
+#pragma unroll
+                    for (int j = 0; j < R4; ++j) {
+                        const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j], qv = q4[u * (Sm::kDk / 4) + 8 * j];
+                        ks2 = __ffma2_rn(make_float2(kv.x, kv.y), S[2 * j], ks2);
+                        qs2 = __ffma2_rn(make_float2(qv.x, qv.y), S[2 * j], qs2);
+                        ks2 = __ffma2_rn(make_float2(kv.z, kv.w), S[2 * j + 1], ks2);
+                        qs2 = __ffma2_rn(make_float2(qv.z, qv.w), S[2 * j + 1], qs2);
+                    }
+                    float ks = ks2.x + ks2.y, qs = qs2.x + qs2.y;
+#pragma unroll
+                    for (int o = 4; o; o >>= 1) {
+                        ks += __shfl_xor_sync(0xffffffffu, ks, o);
+                        qs += __shfl_xor_sync(0xffffffffu, qs, o);
+                    }
+                    const float x = f[Sm::kBeta + u] * (vp[u] - ks);
+                    if (live && p == 4 + u && t + u < n)
+                        Elem<T>::store(yp, fmaf(f[Sm::kE + 5 * u], x, qs));
+#pragma unroll
+                    for (int j = 0; j < R4; ++j) {
+                        const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j];
+                        S[2 * j] = __ffma2_rn(make_float2(kv.x, kv.y), make_float2(x, x), S[2 * j]);
+                        S[2 * j + 1] = __ffma2_rn(make_float2(kv.z, kv.w), make_float2(x, x), S[2 * j + 1]);
+                    }
                 }
-                float4 k[R4];
-                float ks0 = 0.0f, ks1 = 0.0f, qs0 = 0.0f, qs1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < R4; ++j) {
-                    k[j] = k4[8 * j];
-                    const float4 q = q4[8 * j];
-                    ks0 = fmaf(k[j].x, S[4 * j], ks0);
-                    ks1 = fmaf(k[j].y, S[4 * j + 1], ks1);
-                    ks0 = fmaf(k[j].z, S[4 * j + 2], ks0);
-                    ks1 = fmaf(k[j].w, S[4 * j + 3], ks1);
-                    qs0 = fmaf(q.x, S[4 * j], qs0);
-                    qs1 = fmaf(q.y, S[4 * j + 1], qs1);
-                    qs0 = fmaf(q.z, S[4 * j + 2], qs0);
-                    qs1 = fmaf(q.w, S[4 * j + 3], qs1);
-                }
-                float ks = ks0 + ks1, qs = qs0 + qs1;
-#pragma unroll
-                for (int o = 4; o; o >>= 1) {
-                    ks += __shfl_xor_sync(0xffffffffu, ks, o);
-                    qs += __shfl_xor_sync(0xffffffffu, qs, o);
-                }
-                const float d = sc.x;
-                const float u = sc.y * fmaf(-d, ks, v);
-                const float y = fmaf(sc.z, u, d * qs);
-#pragma unroll
-                for (int j = 0; j < R4; ++j) {
-                    const float kv[4] = {k[j].x, k[j].y, k[j].z, k[j].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[4 * j + e] = fmaf(kv[e], u, d * S[4 * j + e]);
-                }
-                if (p == 0 && live)
-                    Elem<T>::store(yp, y);
-                yp += ystep;
+                continue;
             }
+            float2 s2[8] = {}; // S^T k of the four tokens, S^T q of them
+#pragma unroll
+            for (int j = 0; j < R4; ++j) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j], qv = q4[u * (Sm::kDk / 4) + 8 * j];
+                    s2[u] = __ffma2_rn(make_float2(kv.x, kv.y), S[2 * j], s2[u]);
+                    s2[4 + u] = __ffma2_rn(make_float2(qv.x, qv.y), S[2 * j], s2[4 + u]);
+                    s2[u] = __ffma2_rn(make_float2(kv.z, kv.w), S[2 * j + 1], s2[u]);
+                    s2[4 + u] = __ffma2_rn(make_float2(qv.z, qv.w), S[2 * j + 1], s2[4 + u]);
+                }
+            }
+            // lane i < 4 of a column: A_i S^T k_i and what its token writes by itself; 4 + i: A_i S^T q_i
+            const float4 D = *reinterpret_cast<const float4 *>(f + Sm::kD3), E = *reinterpret_cast<const float4 *>(f + Sm::kE + 4 * yi);
+            const float4 ca = *reinterpret_cast<const float4 *>(f + Sm::kC);
+            const float2 cb = *reinterpret_cast<const float2 *>(f + Sm::kC + 4);
+            const float A3 = f[Sm::kA + 3], Ai = f[Sm::kA + yi], bi = f[Sm::kBeta + yi], vi = vp[yi];
+            float s[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                s[u] = s2[u].x + s2[u].y;
+            const float as = Ai * dr_sums<8>(s, p);
+            const float own = bi * (vi - as);
+            const float u0 = __shfl_sync(0xffffffffu, own, 0, 8);
+            const float x1 = __shfl_sync(0xffffffffu, own, 1, 8), x2 = __shfl_sync(0xffffffffu, own, 2, 8),
+                        x3 = __shfl_sync(0xffffffffu, own, 3, 8);
+            const float u1 = fmaf(-ca.x, u0, x1);
+            const float u2 = fmaf(-ca.z, u1, fmaf(-ca.y, u0, x2));
+            const float u3 = fmaf(-cb.y, u2, fmaf(-cb.x, u1, fmaf(-ca.w, u0, x3)));
+            const float w[4] = {D.x * u0, D.y * u1, D.z * u2, u3};
+#pragma unroll
+            for (int i = 0; i < 2 * R4; ++i)
+                S[i] = __fmul2_rn(make_float2(A3, A3), S[i]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int j = 0; j < R4; ++j) {
+                    const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j];
+                    S[2 * j] = __ffma2_rn(make_float2(kv.x, kv.y), make_float2(w[u], w[u]), S[2 * j]);
+                    S[2 * j + 1] = __ffma2_rn(make_float2(kv.z, kv.w), make_float2(w[u], w[u]), S[2 * j + 1]);
+                }
+            }
+            float y = fmaf(E.x, u0, as); // later tokens' u may be infinite or NaN
+            y = yi >= 1 ? fmaf(E.y, u1, y) : y;
+            y = yi >= 2 ? fmaf(E.z, u2, y) : y;
+            y = yi >= 3 ? fmaf(E.w, u3, y) : y;
+            if (live && p >= 4 && t + yi < n)
+                Elem<T>::store(yp, y);
         }
         __syncthreads();
     }
     if (live && a.final_state) {
 #pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) {
-            const int row = 4 * (p + 8 * (i >> 2)) + (i & 3);
+        for (int i = 0; i < 2 * R4; ++i) {
+            const int row = 4 * (p + 8 * (i >> 1)) + 2 * (i & 1);
             if (row < a.dk)
-                a.final_state[sbase + int64_t(row) * a.dv] = S[i];
+                a.final_state[sbase + int64_t(row) * a.dv] = S[i].x;
+            if (row + 1 < a.dk)
+                a.final_state[sbase + int64_t(row + 1) * a.dv] = S[i].y;
         }
     }
 }

@@ -177,6 +177,33 @@ def test_values_that_are_not_finite_stay_where_they_belong(orc, seq, heads_v, dt
             assert_close(y[:, :, 0], ref["outputs"][:, :, 0], TOL[y.dtype], "another head")
 
 
+@pytest.mark.parametrize("dtype,workspace", [("bf16", True), ("bf16", False), ("f32", True)])
+@pytest.mark.parametrize("at", [0, 1, 2, 3, 62, 63, 64])
+def test_growth_of_an_empty_state(orc, dtype, workspace, at):
+    """Decays of e^80 twice over, whose product float32 does not hold, on a state that is
+    still empty: nothing has grown."""
+    inp = make_delta_inputs(1, 100, 1, 2, 64, 32, dtype, seed=3127)
+    inp["g"], inp["beta"] = inp["g"].clone(), inp["beta"].clone()
+    inp["g"][:, at:at + 2] = 80.0
+    inp["beta"][:, :at + 1] = 0.0
+    _check(orc, inp, f"growth at {at}", workspace=workspace)
+
+
+@pytest.mark.parametrize("seq", [1, 2, 3, 4, 5, 31, 32, 33, 36, 37])
+@pytest.mark.parametrize("dv", [4, 30, 600])
+@pytest.mark.parametrize("dk", [16, 72])
+def test_token_form_steps_and_tiles(orc, seq, dv, dk):
+    """Prompts that end inside steps of four tokens and tiles of 32, resets on every place
+    of a step, in narrow and in wide blocks of columns."""
+    inp = make_delta_inputs(2, seq, 1, 1, dk, dv, "f32", seed=3128, h0=True)
+    _check(orc, inp, "no resets")
+    for place in range(min(seq, 4)):
+        reset = torch.zeros(2, seq, dtype=torch.uint8)
+        reset[0, place::8] = 1
+        reset[1, place::5] = 1
+        _check(orc, dict(inp, reset=reset), f"resets from {place}")
+
+
 @pytest.mark.parametrize("seq", [250, 2400])
 def test_chaining_in_place_after_a_nan(orc, seq):
     """The final state may take h0's place in columns that are walked token by token too."""
