@@ -1,6 +1,8 @@
 /*
  * ss_scan.h -- C ABI of libssscan.so: the Mamba-1 selective scan (S6) forward pass
- * and its single-token decode state update on NVIDIA B200 (sm_100a).
+ * and its single-token decode state update on NVIDIA B200 (sm_100a); with them the
+ * gated state scan, the gated delta rule (prompt and decode) and a group norm, each
+ * described at its declaration.
  *
  * What is computed (nnterp documentation, "selective_scan" component: the
  * SelectiveScan class description and the two kernel calls it names,

@@ -1,4 +1,5 @@
-"""B200-native Mamba-1 selective scan (S6) forward and decode state update.
+"""B200-native Mamba-1 selective scan (S6) forward and decode state update, and operators
+beside it: the gated state scan, the gated delta rule, and a per-token group norm.
 
 The compute path lives in the CUDA library ``libssscan.so`` (sources under
 ``csrc/``, C declarations in ``include/ss_scan.h``).  ``ssscan`` is the thin ctypes

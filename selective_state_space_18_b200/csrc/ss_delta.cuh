@@ -368,8 +368,9 @@ struct DeltaUpdateArgs {
 
 constexpr int kDuThreads = 128, kDuCols = 32;
 
-// Six CTAs per SM (for dk up to 128) with packed fp32 arithmetic: 162 us for 256 x 32
-// states of 128 x 128, the rate of a plain copy; 194 us with scalar arithmetic and four.
+// Six CTAs per SM (for dk up to 128) with packed fp32 arithmetic: 162-168 us for 256 x 32
+// states of 128 x 128 (1.07 GB moved) alone, two states in turn, the rate of a plain copy, and
+// 187 us in a run over three states, 88% of it; alone 194 us with scalar arithmetic and four.
 // (Tiles of 64 or 128 columns, 171 and 186 us: fewer CTAs whose phases overlap.)
 // J: row groups of 16 (dk <= 16 J).  VEC: dv a multiple of 4 and a 16-byte aligned state.
 // FULL: dk = 16 J and dv a multiple of 32 as well, so that nothing is guarded (176 us with

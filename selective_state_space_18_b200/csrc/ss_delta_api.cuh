@@ -81,8 +81,9 @@ template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_
 // ---- the chunked form ----------------------------------------------------------------
 
 // Shapes the chunked form takes (bf16; q, k and v as rows of whole 16-byte vectors, which
-// TMA asks for; keys of 8 would leave seven eighths of the tiles empty).  Prompts of up to 16 tokens are walked token by token in less time than
-// the two launches take.
+// TMA asks for; keys of 8 would leave seven eighths of the tiles empty).  Prompts of up to
+// 16 tokens are walked token by token: 8.3 us for 16 heads x 16 tokens, where the two
+// launches of the chunked form take 15.5 us for one chunk of 32 heads.
 bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_dtype_t dtype)
 {
     return dtype == SS_BF16 && dk >= 16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && seq > 16 && seq < (int64_t(1) << 31) - 64 &&
@@ -91,9 +92,9 @@ bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
 
 // Segments of the two-pass walk (1: one pass).  Two passes over 1/S of the chunks, with
 // most SMs holding two walks (1.4 times as long a step each), and the join, against one
-// pass: measured on 256 chunks x 32 heads, 0.94 ms in one pass, 0.62, 0.55, 0.55, 0.56 and
-// 0.59 ms with 4, 6, 7, 9 and 12 segments, and nothing gained on 24 chunks x 36 heads (97
-// to 116 us with 4 to 6 segments, 99 us in one pass).
+// pass: measured on 256 chunks x 32 heads, 0.94 ms in one pass, 0.61, 0.62 and 0.54 ms with 4,
+// 5 and 6 segments (an earlier walk: 0.62, 0.55, 0.55, 0.56 and 0.59 ms with 4, 6, 7, 9 and
+// 12), and nothing gained on 24 chunks x 36 heads (97 to 116 us with 4 to 6, 99 us in one).
 constexpr int64_t kDeltaWalks = 192; // of pass 2
 int64_t delta_segments(int64_t heads, int64_t tiles, int64_t chunks)
 {
@@ -263,8 +264,8 @@ template <typename T, int VEC, int NV, bool CTA> int launch_group_norm(const ss:
 
 // Teams: the fewest lanes of a warp that hold a group in `kMost` vectors each, or a warp
 // with up to eight; beyond that the CTA.  kMost 2 for 16-byte vectors (16384 x 32 groups
-// of 128 bf16 with a gate: 72 us against 78-90 with one vector a lane), 8 for single
-// elements (16384 x 5 groups of 83: 27 us against 31 with a whole warp).
+// of 128 bf16 with a gate, guarded: 72 us against 78-90 with one vector a lane; unguarded
+// 70 us), 8 for single elements (16384 x 5 groups of 83: 27 us against 31 with a whole warp).
 template <typename T, int VEC> int dispatch_group_norm(ss::GroupNormArgs &a, cudaStream_t s)
 {
     constexpr int kMost = VEC == 1 ? 8 : 2;
