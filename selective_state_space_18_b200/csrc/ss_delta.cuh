@@ -35,11 +35,11 @@ struct DeltaArgs {
 //
 // A CTA owns one (batch row, value head) and 16 or 4 of its value columns: columns of the
 // state never meet.  Consumer warps hold the state in registers, a column's dk rows over 8
-// lanes; eight producer warps stage the next 32 tokens, a step of four each, while the
+// or 16 lanes; eight producer warps stage the next 32 tokens, a step of four each, while the
 // consumers walk the current ones, and read the tile after that into registers.
 //
 // What bounds it is the latency of the chain from one state to the next: dot products with
-// the state, their sum over the 8 lanes, the write.  So four tokens 0..3 are taken from one
+// the state, their sum over the lanes, the write.  So four tokens 0..3 are taken from one
 // state S: with a_i their decays, A_i = a_0 .. a_i and D_ij = a_{j+1} .. a_i,
 //   u_i = beta_i (v_i - A_i S^T k_i) - sum_{j<i} beta_i D_ij (k_i . k_j) u_j
 //   y_i = A_i S^T q_i + sum_{j<=i} D_ij (q_i . k_j) u_j
@@ -52,25 +52,26 @@ struct DeltaArgs {
 // All arithmetic is fp32.  It serves fp32 storage, sizes and strides that the tensor-core
 // form does not take, and prompts of a few tokens.
 //
-// Measured (fp32): 2 x 300 tokens x 4 heads of 64: 32.5 us, against 48.7 us one token a
-// step; 4 x 2000 tokens x 4 heads of 64: 202 us against 309 us; 300 tokens x 2 heads of 256:
-// 67 us against 86 us.  What has a few tokens only, or many heads on every SM, loses a
-// little (16 heads of 128 x 4 tokens 6.6 us against 4.7; 256 heads x 300 tokens 659 us
-// against 633).  Rows read a step ahead
-// into registers made it slower (57 us from 40 with keys of 128).
+// Measured (fp32): 2 x 300 tokens x 4 heads of 64: 27.4 us, against 48.7 us one token a
+// step; 4 x 2000 tokens x 4 heads of 64: 219 us against 309 us; 300 tokens x 2 heads of 256:
+// 44.5 us against 86 us.  What has a few tokens only, or many heads on every SM, loses a
+// little (16 heads of 128 x 4 tokens 5.6 us against 4.7; 256 heads x 300 tokens 669 us
+// against 634).
 
-// CW: consumer warps.  They share the SM's path to shared memory, of which a 16-byte read
-// that four columns of a warp have in common takes four turns; where the grid is small, CTAs
-// of one warp each spread that over more SMs.
+// LN: lanes a column.  8 with 16 columns a CTA (four consumer warps), or 16 with 4 columns
+// (two).  A consumer warp issues an instruction in about five cycles, so a step lasts as long
+// as its instructions: 16 lanes halve those of the products, for one more exchange in the
+// sums; and 16-byte reads that the columns of a warp share take four turns of the SM's path to
+// shared memory, which fewer warps crowd less.  Where the grid is small, the narrow form also
+// spreads over more SMs.
 constexpr int kDrTok = 32, kDrStep = 4, kDrProducers = 256;
-constexpr int dr_cols(int cw) { return 4 * cw; }
-constexpr int dr_threads(int cw) { return 32 * cw + kDrProducers; }
-static_assert(kDrProducers / 32 == kDrTok / kDrStep, "a producer warp a step");
+constexpr int dr_cols(int ln) { return ln == 8 ? 16 : 4; }
+constexpr int dr_threads(int ln) { return dr_cols(ln) * ln + kDrProducers; }
 
-template <int R4, int CW> struct DeltaRecSmem { // floats of one staging buffer
+template <int R4, int LN> struct DeltaRecSmem { // floats of one staging buffer
     static constexpr int kDk = 32 * R4; // padded key size
     static constexpr int kVRow = kDrTok + 4;
-    static constexpr int kK = 0, kQ = kDrTok * kDk, kV = 2 * kDrTok * kDk /* [column][token] */, kS = kV + dr_cols(CW) * kVRow;
+    static constexpr int kK = 0, kQ = kDrTok * kDk, kV = 2 * kDrTok * kDk /* [column][token] */, kS = kV + dr_cols(LN) * kVRow;
     // factors of a step: A_i, beta_i, D_3j, a_i (4 each), beta_i D_ij k_i.k_j for ij = 10 20 21 30
     // 31 32, whether it goes token by token, (unused), D_ij q_i.k_j as 4 x 4 rows
     static constexpr int kA = 0, kBeta = 4, kD3 = 8, kDecay = 12, kC = 16, kSingle = 22, kE = 24, kStep = 40;
@@ -78,8 +79,9 @@ template <int R4, int CW> struct DeltaRecSmem { // floats of one staging buffer
     static constexpr size_t kBytes = 2 * size_t(kFloats) * 4;
 };
 
-// Sums of N values over groups of N lanes: lane l of a group is left with that of value l.
-template <int N> __device__ __forceinline__ float dr_sums(float (&v)[N], int lane)
+// Sums of N values over groups of N lanes, `step` apart: lane l of a group is left with that
+// of value l.
+template <int N> __device__ __forceinline__ float dr_sums(float (&v)[N], int lane, int step = 1)
 {
 #pragma unroll
     for (int o = N / 2; o; o >>= 1) {
@@ -87,17 +89,19 @@ template <int N> __device__ __forceinline__ float dr_sums(float (&v)[N], int lan
 #pragma unroll
         for (int i = 0; i < o; ++i) {
             const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * step);
         }
     }
     return v[0];
 }
 
-template <typename T, int R4, int CW>
-__global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const DeltaArgs a)
+template <typename T, int R4, int LN>
+__global__ void __launch_bounds__(dr_threads(LN)) ss_delta_rec_kernel(const DeltaArgs a)
 {
-    using Sm = DeltaRecSmem<R4, CW>;
-    constexpr int kDrCols = dr_cols(CW), kDrConsumers = 32 * CW;
+    using Sm = DeltaRecSmem<R4, LN>;
+    constexpr int RJ = 8 * R4 / LN; // groups of four rows a lane
+    static_assert(RJ * LN == 8 * R4, "the padded key size divides among the lanes");
+    constexpr int kDrCols = dr_cols(LN), kDrConsumers = kDrCols * LN;
     constexpr int kVs = (kDrStep * kDrCols + 31) / 32; // values of v a producer lane loads
     extern __shared__ __align__(16) float dr_sm[];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -222,21 +226,25 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
         return;
     }
 
-    // ======================= consumers: eight lanes a column ===============================
-    const int col = tid >> 3, p = tid & 7;
+    // ======================= consumers: LN lanes a column ==================================
+    const int col = tid / LN, p = tid % LN;
     const bool live = c0 + col < a.dv;
-    float2 S[2 * R4]; // rows 4 (p + 8 j) .. + 3
+    float2 S[2 * RJ]; // rows 4 (p + LN j) .. + 3
     const int64_t sbase = bh * a.dk * a.dv + c0 + col;
 #pragma unroll
-    for (int i = 0; i < 2 * R4; ++i) {
-        const int row = 4 * (p + 8 * (i >> 1)) + 2 * (i & 1);
+    for (int i = 0; i < 2 * RJ; ++i) {
+        const int row = 4 * (p + LN * (i >> 1)) + 2 * (i & 1);
         const bool in = live && a.h0;
         S[i].x = in && row < a.dk ? a.h0[sbase + int64_t(row) * a.dv] : 0.0f;
         S[i].y = in && row + 1 < a.dk ? a.h0[sbase + int64_t(row + 1) * a.dv] : 0.0f;
     }
     __syncthreads();
     const int64_t ystep = int64_t(a.heads_v) * a.dv;
-    const int yi = p & 3; // lane 4 + i of a column writes the output of token i of a step
+    // of the eight sums of a step the lane is left with number `mine`: S^T k of token yi, or
+    // from 4 on S^T q of it, whose output the (first) lane writes
+    constexpr int kSame = LN / 8;
+    const int mine = p / kSame, yi = mine & 3;
+    const bool writes = live && mine >= 4 && p % kSame == 0;
     T *yp = static_cast<T *>(a.y) + ((tok0 + yi) * a.heads_v + h) * a.dv + c0 + col;
     for (int64_t tile = 0; tile < ntiles; ++tile) {
         const float *buf = dr_sm + int(tile & 1) * Sm::kFloats;
@@ -253,11 +261,11 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
                     const float d = f[Sm::kDecay + u];
                     float2 ks2 = make_float2(0.0f, 0.0f), qs2 = ks2;
 #pragma unroll
-                    for (int i = 0; i < 2 * R4; ++i) // a decay of 0 discards the state, whatever it holds
+                    for (int i = 0; i < 2 * RJ; ++i) // a decay of 0 discards the state, whatever it holds
                         S[i] = d == 0.0f ? make_float2(0.0f, 0.0f) : __fmul2_rn(make_float2(d, d), S[i]);
 #pragma unroll
-                    for (int j = 0; j < R4; ++j) {
-                        const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j], qv = q4[u * (Sm::kDk / 4) + 8 * j];
+                    for (int j = 0; j < RJ; ++j) {
+                        const float4 kv = k4[u * (Sm::kDk / 4) + LN * j], qv = q4[u * (Sm::kDk / 4) + LN * j];
                         ks2 = __ffma2_rn(make_float2(kv.x, kv.y), S[2 * j], ks2);
                         qs2 = __ffma2_rn(make_float2(qv.x, qv.y), S[2 * j], qs2);
                         ks2 = __ffma2_rn(make_float2(kv.z, kv.w), S[2 * j + 1], ks2);
@@ -265,16 +273,16 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
                     }
                     float ks = ks2.x + ks2.y, qs = qs2.x + qs2.y;
 #pragma unroll
-                    for (int o = 4; o; o >>= 1) {
+                    for (int o = LN / 2; o; o >>= 1) {
                         ks += __shfl_xor_sync(0xffffffffu, ks, o);
                         qs += __shfl_xor_sync(0xffffffffu, qs, o);
                     }
                     const float x = f[Sm::kBeta + u] * (vp[u] - ks);
-                    if (live && p == 4 + u && t + u < n)
+                    if (writes && yi == u && t + u < n)
                         Elem<T>::store(yp, fmaf(f[Sm::kE + 5 * u], x, qs));
 #pragma unroll
-                    for (int j = 0; j < R4; ++j) {
-                        const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j];
+                    for (int j = 0; j < RJ; ++j) {
+                        const float4 kv = k4[u * (Sm::kDk / 4) + LN * j];
                         S[2 * j] = __ffma2_rn(make_float2(kv.x, kv.y), make_float2(x, x), S[2 * j]);
                         S[2 * j + 1] = __ffma2_rn(make_float2(kv.z, kv.w), make_float2(x, x), S[2 * j + 1]);
                     }
@@ -283,17 +291,17 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
             }
             float2 s2[8] = {}; // S^T k of the four tokens, S^T q of them
 #pragma unroll
-            for (int j = 0; j < R4; ++j) {
+            for (int j = 0; j < RJ; ++j) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j], qv = q4[u * (Sm::kDk / 4) + 8 * j];
+                    const float4 kv = k4[u * (Sm::kDk / 4) + LN * j], qv = q4[u * (Sm::kDk / 4) + LN * j];
                     s2[u] = __ffma2_rn(make_float2(kv.x, kv.y), S[2 * j], s2[u]);
                     s2[4 + u] = __ffma2_rn(make_float2(qv.x, qv.y), S[2 * j], s2[4 + u]);
                     s2[u] = __ffma2_rn(make_float2(kv.z, kv.w), S[2 * j + 1], s2[u]);
                     s2[4 + u] = __ffma2_rn(make_float2(qv.z, qv.w), S[2 * j + 1], s2[4 + u]);
                 }
             }
-            // lane i < 4 of a column: A_i S^T k_i and what its token writes by itself; 4 + i: A_i S^T q_i
+            // A_i S^T k_i and what token i writes by itself, or A_i S^T q_i
             const float4 D = *reinterpret_cast<const float4 *>(f + Sm::kD3), E = *reinterpret_cast<const float4 *>(f + Sm::kE + 4 * yi);
             const float4 ca = *reinterpret_cast<const float4 *>(f + Sm::kC);
             const float2 cb = *reinterpret_cast<const float2 *>(f + Sm::kC + 4);
@@ -302,23 +310,26 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 s[u] = s2[u].x + s2[u].y;
-            const float as = Ai * dr_sums<8>(s, p);
+            float sum = dr_sums<8>(s, p / kSame, kSame);
+            if (LN == 16)
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            const float as = Ai * sum;
             const float own = bi * (vi - as);
-            const float u0 = __shfl_sync(0xffffffffu, own, 0, 8);
-            const float x1 = __shfl_sync(0xffffffffu, own, 1, 8), x2 = __shfl_sync(0xffffffffu, own, 2, 8),
-                        x3 = __shfl_sync(0xffffffffu, own, 3, 8);
+            const float u0 = __shfl_sync(0xffffffffu, own, 0, LN);
+            const float x1 = __shfl_sync(0xffffffffu, own, kSame, LN), x2 = __shfl_sync(0xffffffffu, own, 2 * kSame, LN),
+                        x3 = __shfl_sync(0xffffffffu, own, 3 * kSame, LN);
             const float u1 = fmaf(-ca.x, u0, x1);
             const float u2 = fmaf(-ca.z, u1, fmaf(-ca.y, u0, x2));
             const float u3 = fmaf(-cb.y, u2, fmaf(-cb.x, u1, fmaf(-ca.w, u0, x3)));
             const float w[4] = {D.x * u0, D.y * u1, D.z * u2, u3};
 #pragma unroll
-            for (int i = 0; i < 2 * R4; ++i)
+            for (int i = 0; i < 2 * RJ; ++i)
                 S[i] = __fmul2_rn(make_float2(A3, A3), S[i]);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                for (int j = 0; j < R4; ++j) {
-                    const float4 kv = k4[u * (Sm::kDk / 4) + 8 * j];
+                for (int j = 0; j < RJ; ++j) {
+                    const float4 kv = k4[u * (Sm::kDk / 4) + LN * j];
                     S[2 * j] = __ffma2_rn(make_float2(kv.x, kv.y), make_float2(w[u], w[u]), S[2 * j]);
                     S[2 * j + 1] = __ffma2_rn(make_float2(kv.z, kv.w), make_float2(w[u], w[u]), S[2 * j + 1]);
                 }
@@ -327,15 +338,15 @@ __global__ void __launch_bounds__(dr_threads(CW)) ss_delta_rec_kernel(const Delt
             y = yi >= 1 ? fmaf(E.y, u1, y) : y;
             y = yi >= 2 ? fmaf(E.z, u2, y) : y;
             y = yi >= 3 ? fmaf(E.w, u3, y) : y;
-            if (live && p >= 4 && t + yi < n)
+            if (writes && t + yi < n)
                 Elem<T>::store(yp, y);
         }
         __syncthreads();
     }
     if (live && a.final_state) {
 #pragma unroll
-        for (int i = 0; i < 2 * R4; ++i) {
-            const int row = 4 * (p + 8 * (i >> 1)) + 2 * (i & 1);
+        for (int i = 0; i < 2 * RJ; ++i) {
+            const int row = 4 * (p + LN * (i >> 1)) + 2 * (i & 1);
             if (row < a.dk)
                 a.final_state[sbase + int64_t(row) * a.dv] = S[i].x;
             if (row + 1 < a.dk)

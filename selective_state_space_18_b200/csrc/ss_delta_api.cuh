@@ -43,39 +43,40 @@ int delta_check(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, in
     return SS_OK;
 }
 
-template <typename T, int R4, int CW> int launch_delta_rec_t(const ss::DeltaArgs &a, cudaStream_t s)
+template <typename T, int R4, int LN> int launch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
-    constexpr size_t kSmem = ss::DeltaRecSmem<R4, CW>::kBytes;
-    const int st = ensure_smem(ss::ss_delta_rec_kernel<T, R4, CW>, kSmem, smem_done);
+    constexpr size_t kSmem = ss::DeltaRecSmem<R4, LN>::kBytes;
+    const int st = ensure_smem(ss::ss_delta_rec_kernel<T, R4, LN>, kSmem, smem_done);
     if (st != SS_OK)
         return st;
-    const int64_t tiles = (a.dv + ss::dr_cols(CW) - 1) / ss::dr_cols(CW);
+    const int64_t tiles = (a.dv + ss::dr_cols(LN) - 1) / ss::dr_cols(LN);
     int64_t grid = 0;
     if (!mul_ok(a.batch * a.heads_v, tiles, &grid) || grid > 0x7fffffffLL)
         return SS_ERR_SHAPE;
-    ss::ss_delta_rec_kernel<T, R4, CW><<<unsigned(grid), ss::dr_threads(CW), kSmem, s>>>(a);
+    ss::ss_delta_rec_kernel<T, R4, LN><<<unsigned(grid), ss::dr_threads(LN), kSmem, s>>>(a);
     return launch_status();
 }
 
-// One consumer warp a CTA where all CTAs then run at once, four where they would not: 300
-// tokens x 4 heads of 128, 40 us against 48 us with four; 2 heads of 256, 67 us against 86 us.
-template <typename T, int R4> int launch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
+// Four columns a CTA (16 lanes each) where all CTAs then run at once, sixteen (8 lanes) where
+// they would not: 300 tokens x 4 heads of 128, 34 us against 48 us; 2 heads of 256, 45 us
+// against 86 us.
+template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
 {
     int sms = 0;
     if (device_sm_count(&sms) != SS_OK)
         return SS_ERR_CUDA;
-    const int64_t heads = a.batch * a.heads_v, tiles = (a.dv + ss::dr_cols(1) - 1) / ss::dr_cols(1);
-    return heads <= sms && heads * tiles <= sms ? launch_delta_rec_t<T, R4, 1>(a, s) : launch_delta_rec_t<T, R4, 4>(a, s);
-}
-
-template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_t s)
-{
+    const int64_t heads = a.batch * a.heads_v, tiles = (a.dv + ss::dr_cols(16) - 1) / ss::dr_cols(16);
+    if (heads <= sms && heads * tiles <= sms) {
+        if (a.dk <= 64)
+            return launch_delta_rec<T, 2, 16>(a, s);
+        return a.dk <= 128 ? launch_delta_rec<T, 4, 16>(a, s) : launch_delta_rec<T, 8, 16>(a, s);
+    }
     if (a.dk <= 32)
-        return launch_delta_rec<T, 1>(a, s);
+        return launch_delta_rec<T, 1, 8>(a, s);
     if (a.dk <= 64)
-        return launch_delta_rec<T, 2>(a, s);
-    return a.dk <= 128 ? launch_delta_rec<T, 4>(a, s) : launch_delta_rec<T, 8>(a, s);
+        return launch_delta_rec<T, 2, 8>(a, s);
+    return a.dk <= 128 ? launch_delta_rec<T, 4, 8>(a, s) : launch_delta_rec<T, 8, 8>(a, s);
 }
 
 // ---- the chunked form ----------------------------------------------------------------
