@@ -418,8 +418,9 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *    tokens on the tensor cores.  The state is held in float32 and its operands in 16 bits
  *    of mantissa (final_state follows float32 arithmetic to about 5e-6 of its size), the
  *    outputs' last products take bf16 operands.  Few heads and a long sequence are cut into
- *    segments that run at once.  Columns whose state becomes infinite or NaN are walked
- *    once more token by token, 3 us each: right, but not fast;
+ *    segments that run at once.  Columns whose state or outputs become infinite or NaN on
+ *    the way (writes past about 1e20 under strong decays do, too) are walked once more
+ *    token by token, 3 us each: right, but not fast;
  *  - every other case: token by token, all arithmetic in float32.
  * Results are the same from call to call.
  */

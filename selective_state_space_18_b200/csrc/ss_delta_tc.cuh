@@ -593,6 +593,7 @@ struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kTmem = kBar + 144;
     static constexpr int kAlive = kTmem + 4;  // the walk for M: chunks after which it was not 0
     static constexpr int kDone = kAlive + 4;  // and whether it has become 0
+    static constexpr int kBad = kDone + 4;    // the state or an output is not finite (walks with outputs)
     static constexpr int kBytes = kBar + 256;
 };
 // two CTAs on an SM: 228 KB, 1 KB of it reserved for each
@@ -708,13 +709,14 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t
 }
 
 // The columns n0 .. n0 + 127 of segment `seg` once more, token by token in fp32, where the
-// walk's state has become infinite or NaN.  In products over a chunk 0 times such a value
-// reaches tokens that do not depend on it (those before it, and those behind a reset); it
-// then always stays in the state, which the walk looks at once, at its end.  Here a token
-// only meets what it depends on.  From the state after the segment before when that is
-// finite, or from the first token.  Two syncs a token, two threads a column, the state in
-// shared memory: 2.6 us a token (5.2 ms for 2048 tokens), for inputs that hold such values
-// only.
+// walk's state or an output has become infinite or NaN.  In products over a chunk 0 times such
+// a value reaches tokens that do not depend on it (those before it, and those behind a reset);
+// it then always stays in the state, which the walk looks at once, at its end.  Outputs are
+// looked at as they leave, since they can pass the range of fp32 on the way to finite values:
+// U^T P'^T is up to 2^60 times what it stands for.  Here a token only meets what it depends on.
+// From the state after the segment before when that is finite, or from the first token.  Two
+// syncs a token, two threads a column, the state in shared memory: 2.6 us a token (5.2 ms for
+// 2048 tokens), for inputs that hold or lead to such values only.
 __device__ __noinline__ void delta_rewalk(const DeltaWalkArgs &a, unsigned char *sm, int64_t bh, int seg, int n0)
 {
     const DeltaArgs &d = a.d;
@@ -854,6 +856,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
     volatile int *s_alive = reinterpret_cast<int *>(sm + DwSmem::kAlive);
     volatile int *s_done = reinterpret_cast<int *>(sm + DwSmem::kDone);
+    volatile int *s_bad = reinterpret_cast<int *>(sm + DwSmem::kBad);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const bool issuer = warp == kWarps;
@@ -889,7 +892,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
         for (int i = 13; i < 17; ++i)
             mbar_init(bars + i, kWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *s_alive = *s_done = 0;
+        *s_alive = *s_done = *s_bad = 0;
     }
     if (warp == 0) {
         tmem_alloc(tmem_slot, Sh::kCols);
@@ -904,7 +907,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
     if (!ok && tid == 0)
         atomicOr(status, 1u << kStatusTimeout);
 
-    int bad = 0; // the walk's state is not finite
+    int failed = !ok; // a wait ran out
     if (ok && issuer) {
         // ======================= the issuer warp (one thread works) =======================
         if (elect_one()) {
@@ -1108,7 +1111,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                     mbar_wait(bars + i, (latest >> i) & 1u, nullptr);
         }
         __syncwarp();
-        bad = __syncthreads_or(0);
+        failed = __syncthreads_or(!ok);
     } else if (ok) {
         // ======================= the compute warps =======================================
         // warp w: two tiles m of 16 tensor-memory lanes from row0, group cg of the columns (keys
@@ -1291,6 +1294,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
 #pragma unroll
                     for (int j = 0; j < kTok / 16; ++j) {
                         uint32_t r[8], o[4];
+                        float2 zero2 = make_float2(0.0f, 0.0f);
                         tmem_ld_frag(lanes + (uint32_t(16 * m) << 16) + Sh::kY + (c & 1) * Sh::kYStep + kTok * cg + 16 * j,
                                      r);
 #pragma unroll
@@ -1301,9 +1305,12 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * i + x));
+                                zero2 = __ffma2_rn(make_float2(0.0f, 0.0f), y, zero2);
                                 o[2 * i + x] = pack_bf16x2(y.x, y.y);
                             }
                         }
+                        if (zero2.x + zero2.y != 0.0f) // (0 y is 0 for finite y alone)
+                            *s_bad = 1;
                         // rows of 64 bytes in the 64-byte swizzle: token 8 (2 j + matrix / 2) + lane % 8,
                         // values 16 m + 8 (matrix % 2) ..
                         const int t = 16 * j + 8 * (ln >> 4) + (ln & 7), ch = 2 * m + ((ln >> 3) & 1);
@@ -1395,11 +1402,12 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
                         sum = __ffma2_rn(make_float2(0.0f, 0.0f), H[m][k][x], sum);
-            bad = sum.x != 0.0f || sum.y != 0.0f;
+            if (sum.x != 0.0f || sum.y != 0.0f)
+                *s_bad = 1;
         }
         __syncwarp();
-        bad = __syncthreads_or(bad); // before h0's place may take the final state
-        if (ok && to && !(outs && bad)) {
+        failed = __syncthreads_or(!ok); // before h0's place may take the final state
+        if (ok && to && !*s_bad) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1419,7 +1427,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
     tc_fence_after();
     if (warp == 0)
         tmem_dealloc(tmem, Sh::kCols);
-    if (bad)
+    if (*s_bad && !failed)
         delta_rewalk(a, sm, bh, seg, n0);
 }
 
