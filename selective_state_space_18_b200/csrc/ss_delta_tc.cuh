@@ -1141,7 +1141,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                     const bool in = from && key < a.dk && vc < cols; // (dk is even)
                     const int64_t o = sofs + int64_t(8 * k) * cols + 16 * m + 8 * x;
                     H[m][k][x] = make_float2(in ? from[o] : 0.0f, in ? from[o + cols] : 0.0f);
-                    if (for_m) // the identity
+                    if (for_m && key < a.dk) // the identity (padded keys are never updated: they stay 0)
                         H[m][k][x] = make_float2(key == vc ? 1.0f : 0.0f, key + 1 == vc ? 1.0f : 0.0f);
                     if (in && a.pass == 1 && seg == 0 && a.seg_h0) {
                         a.seg_h0[bh * a.dk * a.dv + o] = H[m][k][x].x;

@@ -47,3 +47,19 @@ def test_large_and_small_writes(orc, seq, heads_v, dtype, workspace, power):
     y, fs = _scan(inp, scale=1.0, qk_l2norm=True, workspace=workspace)
     assert_close(y.double() * 2.0 ** -power, ref["outputs"], TOL[y.dtype], "outputs")
     assert_close(fs.double() * 2.0 ** -power, ref["final_state"], TOL[F32], "final state")
+
+
+@pytest.mark.parametrize("dk", [16, 24, 64, 72, 96, 112, 128])
+def test_maps_of_segments_that_forget_are_zero(dk):
+    """36 chunks of one head are three segments.  With a decay of e^-1 a token the middle one's
+    map from state to state is exactly 0 after two chunks, whatever the key size: the last word
+    of the workspace says so, and the walk for the map ends there."""
+    inp = _cuda_dict(make_delta_inputs(1, 36 * 64, 1, 1, dk, 64, "bf16", seed=3610, h0=True))
+    need = ssscan.ss_delta_workspace_bytes(1, 36 * 64, 1, 1, dk, 64)
+    ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    flag = ws[need - 4:need].view(torch.int32)
+    for g, zero in ((-1.0, 1), (-1e-3, 0)):
+        inp["g"] = torch.full_like(inp["g"], g)
+        ssscan.ss_delta_scan(**inp, qk_l2norm=True, workspace=ws)
+        assert flag.item() == zero, g
+    assert bool((ws[need:] == 0xff).all())
