@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
             const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
             if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
                 cut = tid > 0; // (at the first token: see above)
-            } else if (tid > 0 || chunk > 0 || d.h0) {
+            } else if (tid > 0 || chunk > 0 || d.h0 || g2 != g2) { // (an empty state has nothing to lose)
                 gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
                 gl = g2 - gh;
             }

@@ -63,3 +63,75 @@ def test_maps_of_segments_that_forget_are_zero(dk):
         ssscan.ss_delta_scan(**inp, qk_l2norm=True, workspace=ws)
         assert flag.item() == zero, g
     assert bool((ws[need:] == 0xff).all())
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "h0"])
+@pytest.mark.parametrize("seq,heads_v,dtype,workspace", FORMS)
+def test_values_that_are_not_finite_arrive(orc, seq, heads_v, dtype, workspace, where, value):
+    """From the token of an infinity or NaN to the next reset, outputs (and the final state
+    where no reset comes) are finite exactly where the definition's are; in other value columns
+    of the head that holds it in v or h0 they are what they are without it."""
+    if where == "g" and not math.isnan(value):
+        pytest.skip("log decays lie below infinity, and minus infinity is a decay of 0")
+    for at, cut, h0 in ((200, 201, True), (100, 180, True), (0, 70, True), (0, 70, False), (seq - 1, None, True)):
+        if where == "h0" and not h0:
+            continue
+        clean = make_delta_inputs(1, seq, 1, heads_v, 64, 136, dtype, seed=3620, h0=h0)
+        clean["reset"] = torch.zeros(1, seq, dtype=torch.uint8)
+        if cut is not None:
+            clean["reset"][0, cut] = 1
+        inp = {k: (None if v is None else v.clone()) for k, v in clean.items()}
+        if where == "h0":
+            inp["h0"][0, -1, 5, -1] = value
+        else:
+            inp[where][0, at].view(-1)[-1] = value
+        y, fs = _scan(inp, scale=1.0, qk_l2norm=True, workspace=workspace)
+        ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
+        first = 0 if where == "h0" else at
+        finite = torch.from_numpy(ref["outputs"][:, first:cut]).isfinite()
+        assert torch.equal(y[:, first:cut].isfinite(), finite), f"outputs from {first} to {cut}"
+        assert not finite.all()
+        if cut is None:
+            assert torch.equal(fs.isfinite(), torch.from_numpy(ref["final_state"]).isfinite()), "final state"
+        if where in ("v", "h0"):
+            ref = orc.delta_scan(**clean, scale=1.0, qk_l2norm=True)
+            assert_close(y[..., :-1], ref["outputs"][..., :-1], TOL[y.dtype], "other columns")
+            assert_close(fs[..., :-1], ref["final_state"][..., :-1], TOL[F32], "other columns, final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta", "h0"])
+def test_values_that_are_not_finite_in_a_decode_step(orc, dtype, where, value):
+    """The same of one step: in the head that holds it, and in v or h0 in its column alone."""
+    if where == "g" and value == math.inf:
+        pytest.skip("log decays lie below infinity")
+    inp = make_delta_inputs(3, 1, 1, 2, 64, 72, dtype, seed=3630, h0=True)
+    clean = {k: (None if v is None else v.clone()) for k, v in inp.items()}
+    inp[where][1].view(-1)[-1] = value
+    d = _cuda_dict(inp)
+    y = ssscan.ss_delta_update(d["h0"], *(d[n][:, 0] for n in ("q", "k", "v", "g", "beta")), scale=1.0, qk_l2norm=True)
+    ref, well = (orc.delta_scan(**x, scale=1.0, qk_l2norm=True) for x in (inp, clean))
+    for out, name in ((y.cpu(), "outputs"), (d["h0"].cpu(), "final_state")):
+        r = torch.from_numpy(ref[name]).view(out.shape)
+        w = torch.from_numpy(well[name]).view(out.shape)
+        assert torch.equal(out.isfinite(), r.isfinite()), name
+        f = r.isfinite()
+        assert_close(out[f], w[f].numpy(), TOL[out.dtype], name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [8, 24, 33, 640, 2900])
+def test_norm_keeps_a_nan_in_its_group(dtype, size):
+    """Groups side by side in a warp, in a warp each and in a CTA each: the others of a row
+    and the other rows give the same bits with a NaN beside them as without."""
+    t = BF16 if dtype == "bf16" else F32
+    x = torch.randn(9, 5 * size, generator=torch.Generator().manual_seed(3640)).to(t).cuda()
+    ref = ssscan.ss_group_norm(x, 5, activation="silu").view(9, 5, size)
+    bad = x.clone()
+    bad[4, 2 * size + 3] = math.nan
+    y = ssscan.ss_group_norm(bad, 5, activation="silu").view(9, 5, size)
+    assert bool(y[4, 2].isnan().all())
+    y[4, 2] = ref[4, 2]
+    assert torch.equal(y, ref)
