@@ -48,8 +48,10 @@
 // output itself being 1.7e-3).
 //
 // Decays.  The cumulative log2 decays are kept as a part of multiples of 1/64, which sums
-// and differences exactly, and a remainder below 1/128 a token, so the decay between two
-// tokens is exact to 1e-7 however much the chunk decays in all.  A token whose decay is
+// and differences exactly, and a remainder below 1/128 a token, each with an exponential of its
+// own, so the factors from the chunk's start or to its end are right to 7e-7 however much the
+// chunk decays in all (1.7e-6 over 2^-53 with one exponential of the sum, and worse with the
+// roundings of g log2(e) added up).  A token whose decay is
 // zero in fp32 (a reset, -inf, below 2^-160) cuts: cut counts tell which pairs it parts.
 // A cut at a chunk's first token leaves the chunk itself alone: the chunk before it hands
 // on a state of zero (and h0 is not read).  A sequence without h0 begins the same way, so
@@ -66,6 +68,7 @@
 namespace ss {
 
 constexpr int kDcChunk = 64; // tokens per chunk
+constexpr float kDcLog2eRest = float(1.4426950408889634 - double(kLog2e)); // log2(e) beyond kLog2e
 
 // A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63 and the mode: 0 for
 // P', 1 for P and scaled rows of Q), then P' or P.  A matrix is
@@ -254,12 +257,13 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         if (tid < n) {
             const int64_t gi = (tok0 + tid) * d.heads_v + h;
             be = d.beta ? __ldg(d.beta + gi) : 1.0f;
-            const float g2 = d.g ? __ldg(d.g + gi) * kLog2e : 0.0f;
+            const float g = d.g ? __ldg(d.g + gi) : 0.0f, g2 = g * kLog2e;
             if ((d.reset && d.reset[tok0 + tid]) || g2 < -160.0f) {
                 cut = tid > 0; // (at the first token: see above)
             } else if (tid > 0 || chunk > 0 || d.h0 || g2 != g2) { // (an empty state has nothing to lose)
                 gh = rintf(g2 * 64.0f) * (1.0f / 64.0f);
-                gl = g2 - gh;
+                // (g log2(e) - gh, without the roundings of the product and of log2(e))
+                gl = fmaf(g, kDcLog2eRest, fmaf(g, kLog2e, -gh));
             }
         }
 #pragma unroll
@@ -354,18 +358,19 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
     // whether E and 1 / E are in range over the whole chunk
     const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f)));
     if (tid < 64) {
-        const float e = cut ? 0.0f : ex2(gh + gl);
+        // (in two factors: the sum of both parts would be rounded, 60 to 2^-19)
+        const float e = cut ? 0.0f : ex2(gh) * ex2(gl);
         const float r = sR[tid];
         reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
         // the decays factor through the chunk's start where E is in range
-        sF[tid] = r * ex2(-(gh + gl));
+        sF[tid] = r * (ex2(-gh) * ex2(-gl));
         sB[tid] = be * r * e;
         reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
         const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
         reinterpret_cast<float *>(blk + kDcW)[tid] =
-            hand && cut == sN[63] ? r * ex2((sGh[63] - gh) + (sGl[63] - gl)) : 0.0f;
+            hand && cut == sN[63] ? r * (ex2(sGh[63] - gh) * ex2(sGl[63] - gl)) : 0.0f;
         if (tid == 0) {
-            reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63] + sGl[63]);
+            reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63]) * ex2(sGl[63]);
             reinterpret_cast<float *>(blk + kDcE)[1] = direct ? 1.0f : 0.0f;
         }
     }

@@ -135,3 +135,23 @@ def test_norm_keeps_a_nan_in_its_group(dtype, size):
     assert bool(y[4, 2].isnan().all())
     y[4, 2] = ref[4, 2]
     assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("decay", ["constant", "random", "growing", "strong"])
+def test_factors_of_a_chunk(decay):
+    """The decays from a chunk's start to its tokens (c and s in the workspace block, for unit
+    scale and no norm), from them to its end (w), and over it, against 64 bits.  Two
+    exponentials with a relative error of up to 2^-22 each, their product (2^-24), and up to
+    eight roundings of a sum below one half (2^-26 each, times ln 2): 6.2e-7 in all."""
+    inp = make_delta_inputs(1, 64, 1, 1, 128, 128, "bf16", seed=3650)
+    u = torch.rand(inp["g"].shape, generator=torch.Generator().manual_seed(3651))
+    inp["g"] = {"constant": torch.full_like(u, -0.63), "random": -0.9 * u, "growing": 0.3 + 0.3 * u,
+                "strong": -3.0 * u}[decay]
+    need = ssscan.ss_delta_workspace_bytes(1, 64, 1, 1, 128, 128)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    ssscan.ss_delta_scan(**_cuda_dict(dict(inp, h0=torch.zeros(1, 1, 128, 128))), scale=1.0, workspace=ws)
+    c, w, s, e = ws[2 * 6144:2 * 6144 + 4 * 256].view(F32).double().cpu().view(4, 64)
+    G = inp["g"].double().view(-1).cumsum(0)
+    for got, log, what in ((c, G, "c"), (s, G, "s"), (w, G[-1] - G, "w"), (e[:1], G[-1:], "E_63")):
+        rel = ((got - log.exp()) / log.exp()).abs()[log > -86.0]   # (below: under float32's normal range)
+        assert float(rel.max() if rel.numel() else 0.0) <= 6.2e-7, what
