@@ -155,3 +155,49 @@ def test_factors_of_a_chunk(decay):
     for got, log, what in ((c, G, "c"), (s, G, "s"), (w, G[-1] - G, "w"), (e[:1], G[-1:], "E_63")):
         rel = ((got - log.exp()) / log.exp()).abs()[log > -86.0]   # (below: under float32's normal range)
         assert float(rel.max() if rel.numel() else 0.0) <= 6.2e-7, what
+
+
+@pytest.mark.parametrize("shape", [(1, 500, 1, 2, 128, 128), (2, 700, 1, 2, 64, 64), (1, 300, 2, 160, 96, 64),
+                                   (1, 3000, 1, 2, 128, 136), (1, 2500, 2, 4, 96, 128)])
+@pytest.mark.parametrize("slow", [False, True])
+def test_error_of_the_chunked_form_in_norm(orc, shape, slow):
+    """Rounding a value to bfloat16 costs 1.66e-3 of the norm (half a step, uniform over the
+    mantissa); keeping the remainder in bfloat16 too leaves the square of it, 2.8e-6.  The
+    state: five such splits on the way of a chunk (H, R, T, w o U and the product of two
+    remainders that is left out), 6.2e-6 as they fall, tripled for the chunks that a state
+    remembers.  The outputs: the rounding of their own and of H in Q H, and of P and U in P U,
+    where the terms of a sum may be half as large again as the sum in norm:
+    1.66e-3 sqrt(1 + 1 + 2 x 1.5^2) = 4.2e-3.  A lost remainder would cost the state 1e-3."""
+    inp = make_delta_inputs(*shape, "bf16", seed=3660 + sum(shape), h0=True)
+    if slow:
+        inp["g"] = inp["g"] * 1e-2
+    y, fs = _scan(inp, scale=1.0, qk_l2norm=True)
+    ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
+    for got, want, tol, what in ((y, ref["outputs"], 4.2e-3, "outputs"), (fs, ref["final_state"], 1.9e-5, "state")):
+        want = torch.from_numpy(want)
+        err = float((got.double() - want).norm() / want.norm())
+        assert err <= tol, f"{what}: {err:.2e}"
+
+
+@pytest.mark.parametrize("seq,heads_v,dtype,workspace", FORMS)
+def test_largest_growth(orc, seq, heads_v, dtype, workspace):
+    """A decay of e^88.5, close to the largest that float32 holds, on a state that is still
+    empty, and one of e^40 on a state of 1e-20."""
+    inp = make_delta_inputs(1, seq, 1, heads_v, 64, 32, dtype, seed=3670)
+    inp["g"], inp["beta"] = inp["g"].clone(), inp["beta"].clone()
+    inp["g"][:, 10] = inp["g"][:, 75] = 88.5
+    inp["beta"][:, :76] = 0.0
+    _check_forms(orc, inp, workspace, 1.0)
+    inp = make_delta_inputs(1, seq, 1, heads_v, 64, 32, dtype, seed=3671, h0=True)
+    inp["g"], inp["h0"] = inp["g"].clone(), inp["h0"] * 1e-20
+    inp["g"][:, :20] = -0.01
+    inp["g"][:, 20] = 40.0
+    inp["beta"] = torch.cat((torch.zeros_like(inp["beta"][:, :21]), inp["beta"][:, 21:]), 1)
+    _check_forms(orc, inp, workspace, 1.0)
+
+
+def _check_forms(orc, inp, workspace, scale):
+    y, fs = _scan(inp, scale=scale, qk_l2norm=True, workspace=workspace)
+    ref = orc.delta_scan(**inp, scale=scale, qk_l2norm=True)
+    assert_close(y, ref["outputs"], TOL[y.dtype], "outputs")
+    assert_close(fs, ref["final_state"], TOL[F32], "final state")
