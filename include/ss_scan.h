@@ -415,12 +415,13 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  * Two forms:
  *  - bf16 with dk a multiple of 8 from 16 to 128, dv a multiple of 8, more than 16 tokens,
  *    16-byte aligned tensors, strides that are multiples of 8 and a workspace: chunks of 64
- *    tokens on the tensor cores.  The state is held in float32 and its operands in 16 bits
- *    of mantissa (final_state follows float32 arithmetic to about 5e-6 of its size), the
- *    outputs' last products take bf16 operands.  Few heads and a long sequence are cut into
- *    segments that run at once.  Columns whose state or outputs become infinite or NaN on
- *    the way (writes past about 1e20 under strong decays do, too) are walked once more
- *    token by token, 3 us each: right, but not fast;
+ *    tokens on the tensor cores.  The state is held in float32 and computed operands in 16
+ *    bits of mantissa: final_state follows float32 arithmetic to about 5e-6 of its size (to
+ *    4e-5 with keys that resemble each other, to 1e-3 where beta |k|^2 nears 2 as well), and
+ *    outputs are off by little more than their own rounding.  Few heads and a long sequence
+ *    are cut into segments that run at once.  Columns whose state or outputs become infinite
+ *    or NaN on the way (writes past about 1e20 under strong decays do, too) are walked once
+ *    more token by token, 2.6 us each: right, but not fast;
  *  - every other case: token by token, all arithmetic in float32.
  * Results are the same from call to call.
  */

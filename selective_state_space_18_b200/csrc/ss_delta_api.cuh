@@ -134,10 +134,10 @@ int launch_delta_walk_t(const ss::DeltaWalkArgs &w, const ss::DeltaWalkMaps &map
                         cudaStream_t s)
 {
     static std::atomic<uint64_t> smem_done{0};
-    const int st = ensure_smem(ss::ss_delta_walk_kernel<G>, size_t(ss::DwSmem::kBytes), smem_done);
+    const int st = ensure_smem(ss::ss_delta_walk_kernel<G>, size_t(ss::DwSmem<G>::kBytes), smem_done);
     if (st != SS_OK)
         return st;
-    ss::ss_delta_walk_kernel<G><<<grid, ss::DwShape<G>::kThreads, ss::DwSmem::kBytes, s>>>(w, maps, status);
+    ss::ss_delta_walk_kernel<G><<<grid, ss::DwShape<G>::kThreads, ss::DwSmem<G>::kBytes, s>>>(w, maps, status);
     return launch_status();
 }
 

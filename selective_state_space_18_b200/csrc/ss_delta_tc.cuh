@@ -16,8 +16,8 @@
 //
 // The preparation (ss_delta_prep_kernel, one CTA per chunk and value head) needs no state:
 // K K^T and Q K^T, the decays, T = (I + A)^{-1} diag(beta) by substitution in fp32, and
-// per chunk and value head a 19 KB block of the workspace: T (split into a bf16 high part
-// and a bf16 remainder) and P (bf16) as operand tiles, c, w, s and E_63.
+// per chunk and value head a 25 KB block of the workspace: T and P (each split into a bf16
+// high part and a bf16 remainder) as operand tiles, c, w, s and E_63.
 //
 // The walk (ss_delta_walk_kernel, one CTA per head and 128 value columns) keeps H in fp32
 // registers, transposed: tensor-memory lane = value column.  Every product then takes its
@@ -25,11 +25,13 @@
 // through shared memory, and its right operand straight from the TMA tiles of k and q:
 //   KH^T [128 x 64]  = H^T K^T              R^T = V^T - KH^T diag(c)
 //   U^T  [128 x 64]  = R^T T^T              (only the blocks of T on and below the diagonal)
-//   Y^T  [128 x 64]  = (H^T Q^T + U^T P'^T) diag(s),   P'_ij = P_ij / s_i = r_j D_ij/E_i q_i.k_j
+//   Y^T  [128 x 64]  = (H^T Q^T + (w o U)^T P'^T) diag(s),   P'_ij = q_i.k_j / E_63  (j <= i)
 //   dH^T [128 x dk]  = (w o U)^T K          H = E_63 H + dH
-// P' is only in range where the chunk's decays are: with a cut in the chunk, or decays
-// beyond 2^-60 in all, the walk scales the rows of Q by s in shared memory instead and
-// takes P itself (the block says which).
+// since P_ij = s_i P'_ij w_j without a cut in the chunk.  One operand serves both products.
+// P' and w are only in range where the chunk's decays are: with a cut in the chunk, or decays
+// beyond 2^-60 in all, U^T is kept beside w o U, P' is P_ij / m_i, and the walk scales the rows
+// of Q by 2^e_i in shared memory, for s_i = m_i 2^e_i: exactly, with m_i left for the end (the
+// block says which).
 //
 // Few heads and a long prompt leave most SMs without a walk.  The sequence is then cut into
 // segments that are walked at once, in two passes ("s6_reset" blog draft, Associative
@@ -43,9 +45,11 @@
 // Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
 // state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
 // products summed in fp32, so the final state follows fp32 arithmetic to about 5e-6 of
-// its size.  On the way to the outputs, which are rounded to bf16 anyway, H, P and U enter
-// rounded to bf16 once each (output error 2.7e-3 of the norm in all, the rounding of the
-// output itself being 1.7e-3).
+// its size.  So do those on the way to the outputs (H, w o U or U, P'): where keys resemble each
+// other the terms of P U are many times its sum, and operands of 8 bits were off by up to 0.13
+// in outputs of order one.  Only in chunks with a cut or strong decays does H enter H^T Q^T
+// rounded to bf16 (two walks an SM: its remainder has made room for U^T).  Output error 1.7e-3
+// of the norm, which is the rounding of the output itself, and up to 2.4e-3 in such chunks.
 //
 // Decays.  The cumulative log2 decays are kept as a part of multiples of 1/64, which sums
 // and differences exactly, and a remainder below 1/128 a token, each with an exponential of its
@@ -70,8 +74,8 @@ namespace ss {
 constexpr int kDcChunk = 64; // tokens per chunk
 constexpr float kDcLog2eRest = float(1.4426950408889634 - double(kLog2e)); // log2(e) beyond kLog2e
 
-// A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63 and the mode: 0 for
-// P', 1 for P and scaled rows of Q), then P' or P.  A matrix is
+// A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63 and the mode: 0, or 1 for
+// cuts and strong decays), then P' hi, P' lo.  A matrix is
 // four slices ks of 32-byte rows in the 32-byte swizzle: columns 16 ks .. 16 ks + 15, rows
 // 0..63 of the first two slices and 32..63 of the last two (the rest is above the diagonal
 // and 0).  Products with it accumulate into two halves of 32 tokens each, always with
@@ -82,8 +86,16 @@ __host__ __device__ constexpr int dc_slice(int ks) { return ks < 2 ? 2048 * ks :
 constexpr int kDcThi = 0, kDcTlo = kDcMat, kDcC = 2 * kDcMat, kDcW = kDcC + 256, kDcS = kDcW + 256, kDcE = kDcS + 256,
               kDcP = kDcE + 256;
 constexpr int kDcHead = kDcP;                     // the part loaded ahead of P
-constexpr int kDcBlockBytes = kDcP + kDcMat;      // workspace per chunk and value head
-static_assert(kDcHead % 1024 == 0 && kDcBlockBytes == 19456, "workspace block");
+constexpr int kDcBlockBytes = kDcP + 2 * kDcMat;  // workspace per chunk and value head
+static_assert(kDcHead % 1024 == 0 && kDcBlockBytes == 25600, "workspace block");
+
+// s = m 2^e: the power of two (0 for 0 and below float32's normal range) and m (1 to 2 in
+// size, with the sign), whose product is s, or 0 there.
+__device__ __forceinline__ float dc_power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7f800000u); }
+__device__ __forceinline__ float dc_mantissa(float s)
+{
+    return __uint_as_float((__float_as_uint(s) & 0x807fffffu) | 0x3f800000u);
+}
 
 // Byte offset of element (i, j) of a matrix in its slices (i >= 32 when j >= 32): the
 // 16-byte half of a 32-byte row is XORed with bit 2 of the row (address bit 4 with bit 7).
@@ -155,10 +167,10 @@ constexpr int kDpRow = 136;   // elements between rows of the q and k tiles (272
 constexpr int kDpDRow = 20;   // floats between rows of a diagonal block
 struct DeltaPrepSmem {        // the image, T_kj^T and the diagonal blocks take the place of the tiles
     static constexpr int kK = 0, kQ = kDcChunk * kDpRow * 2;
-    static constexpr int kImg = 0;                    // T hi, T lo, P
-    static constexpr int kTT = kImg + 3 * kDcMat;     // T_kj^T, k < 3, as fragments: [6 blocks][32 lanes][8]
+    static constexpr int kImg = 0;                    // T hi, T lo, P' hi, P' lo
+    static constexpr int kTT = kImg + 4 * kDcMat;     // T_kj^T, k < 3, as fragments: [6 blocks][32 lanes][8]
     static constexpr int kDiag = kTT + 6 * 1024;      // [4 warps][16][kDpDRow]
-    static constexpr int kScal = 2 * kQ; // per token: Gh, Gl, cut count, r, p, beta, r / E, beta r E (64 floats each)
+    static constexpr int kScal = 2 * kQ + 1024; // per token: Gh, Gl, cut count, r, p, beta, r / E, beta r E (64 floats each)
     static constexpr int kBytes = kScal + 8 * 256 + 16;
     static_assert(kDiag + 4 * 16 * kDpDRow * 4 <= kScal, "inside the tiles");
 };
@@ -355,8 +367,8 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         sN[tid] = cut;
         sBeta[tid] = be;
     }
-    // whether E and 1 / E are in range over the whole chunk
-    const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f)));
+    // whether the state is discarded in the chunk or behind it, or E leaves the range of 1 / E
+    const bool direct = __syncthreads_or(tid < 64 && (cut || !(fabsf(gh + gl) <= 60.0f))) || sRed[3] == 0.0f;
     if (tid < 64) {
         // (in two factors: the sum of both parts would be rounded, 60 to 2^-19)
         const float e = cut ? 0.0f : ex2(gh) * ex2(gl);
@@ -365,8 +377,11 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         // the decays factor through the chunk's start where E is in range
         sF[tid] = r * (ex2(-gh) * ex2(-gl));
         sB[tid] = be * r * e;
-        reinterpret_cast<float *>(blk + kDcS)[tid] = sP[tid] * e;
         const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
+        const float se = sP[tid] * e;
+        reinterpret_cast<float *>(blk + kDcS)[tid] = se;
+        if (direct)
+            sP[tid] = sP[tid] / dc_mantissa(se);
         reinterpret_cast<float *>(blk + kDcW)[tid] =
             hand && cut == sN[63] ? r * (ex2(sGh[63] - gh) * ex2(sGl[63] - gl)) : 0.0f;
         if (tid == 0) {
@@ -378,12 +393,13 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
     // ---- A, in place of K K^T, and P ---------------------------------------------------
     {
         const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
-        // rows scale by bi (A) and pi (P); d2(j, x) are the factors of columns j and j + 1
-        auto scale = [&](float2 bi, float2 pi, auto d2) {
+        // rows scale by bi (A) and pi (P'); d2(j, x) are A's factors of columns j and j + 1, and
+        // those of P' in chunks with cuts or strong decays
+        auto scale = [&](float2 bi, float2 pi, bool both, auto d2) {
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb) {
                 if (jb <= (warp | 1)) { // (above the diagonal: zeros of the slices)
-                    uint32_t w[4];
+                    uint32_t w[4], wl[4];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         const int nt = 2 * jb + n, j = 8 * nt + j0;
@@ -394,7 +410,8 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
                             const float2 f = d2(j, x);
                             float2 av = __fmul2_rn(__fmul2_rn(f, make_float2(b1, b1)),
                                                    make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
-                            float2 pv = __fmul2_rn(__fmul2_rn(f, make_float2(p1, p1)),
+                            const float2 pf = make_float2(p1, p1);
+                            float2 pv = __fmul2_rn(both ? __fmul2_rn(f, pf) : pf,
                                                    make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
                             if (jb >= warp) { // on or above the diagonal blocks
                                 av.x = j < i ? av.x : 0.0f;
@@ -404,20 +421,22 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
                             }
                             kk[nt][2 * x] = av.x;
                             kk[nt][2 * x + 1] = av.y;
-                            w[2 * n + x] = pack_bf16x2(pv.x, pv.y);
+                            split_bf16x2(pv.x, pv.y, w[2 * n + x], wl[2 * n + x]);
                         }
                     }
                     dp_store_block(img + 2 * kDcMat, warp, jb, lane, w);
+                    dp_store_block(img + 3 * kDcMat, warp, jb, lane, wl);
                 }
             }
         };
         if (!direct) {
-            scale(make_float2(sB[i0], sB[i0 + 8]), make_float2(1.0f, 1.0f),
+            const float inv = ex2(-sGh[63]) * ex2(-sGl[63]); // 1 / E_63
+            scale(make_float2(sB[i0], sB[i0 + 8]), make_float2(inv, inv), false,
                   [&](int j, int) { return *reinterpret_cast<const float2 *>(sF + j); });
         } else {
             const float gih[2] = {sGh[i0], sGh[i0 + 8]}, gil[2] = {sGl[i0], sGl[i0 + 8]};
             const int ni[2] = {sN[i0], sN[i0 + 8]};
-            scale(make_float2(sBeta[i0] * sR[i0], sBeta[i0 + 8] * sR[i0 + 8]), make_float2(sP[i0], sP[i0 + 8]),
+            scale(make_float2(sBeta[i0] * sR[i0], sBeta[i0 + 8] * sR[i0 + 8]), make_float2(sP[i0], sP[i0 + 8]), true,
                   [&](int j, int x) {
                       return make_float2(
                           sN[j] == ni[x] ? sR[j] * ex2((gih[x] - sGh[j]) + (gil[x] - sGl[j])) : 0.0f,
@@ -550,7 +569,7 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
                      "r"(2 * kDcMat)
                      : "memory");
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(blk + kDcP),
-                     "r"(img + 2 * kDcMat), "r"(kDcMat)
+                     "r"(img + 2 * kDcMat), "r"(2 * kDcMat)
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -566,8 +585,8 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
 //
 // G: groups of four compute warps, each with a G-th of the columns: 2 (two CTAs per SM) or
 // 4 (one CTA per SM).  A CTA alone on its SM has room for Y^T beside the rest, in two places
-// that alternate: H^T Q^T follows KH^T at once, U^T P^T follows dH^T, and the outputs leave
-// after the state is handed on, while the next chunk's first product runs.  With two CTAs
+// that alternate: H^T Q^T follows KH^T at once, (w o U)^T P'^T follows dH^T, and the outputs
+// leave after the state is handed on, while the next chunk's first product runs.  With two CTAs
 // Y^T takes R^T's place, between U^T and dH^T.
 template <int G> struct DwShape {
     static constexpr int kWarps = 4 * G;              // compute warps
@@ -578,23 +597,27 @@ template <int G> struct DwShape {
     static constexpr uint32_t kCols = kLate ? 512 : 256; // tensor memory
     static constexpr uint32_t kY = kLate ? 256 : 128;    // Y^T
     static constexpr uint32_t kYStep = kLate ? 64 : 0;   // from Y^T of even chunks to that of odd ones
-    static constexpr uint32_t kU = kLate ? 384 : 72;     // U^T rounded, for Y: 16 tokens 16 columns apart
+    // U^T for Y in chunks with cuts or strong decays, high parts and remainders: 8 columns of
+    // 16 tokens, 16 columns apart
+    static constexpr uint32_t kUh = kLate ? 384 : 72, kUl = kLate ? 392 : 8;
 };
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
 // then R^T over it in the same form (16 columns per 16 tokens).  D2: U^T, then
-// (w o U)^T over it.  U^T rounded, for Y, lies in the places of remainders of H that KH^T has
-// read, or has its own where there is room.
+// (w o U)^T over it.  U^T lies in the places of remainders of H that KH^T has read, or has its
+// own where there is room.
 constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192;
 
-struct DwSmem { // from a 1024-byte aligned base
+template <int G> struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kK = 0;                // k chunk: 2 stages of two [64 tokens x 64 keys] tiles
     static constexpr int kQ = kK + 2 * 16384;   // q chunk: two tiles
     static constexpr int kV = kQ + 16384;       // v chunk: two [64 tokens x 64 values] tiles
-    static constexpr int kY = kV + 16384;       // outputs: a tile of [kTok tokens x 32 values] per compute warp
-    static constexpr int kB = kY + 16384;       // workspace blocks up to P: 2 stages
-    static constexpr int kP = kB + 2 * kDcHead; // P
-    static constexpr int kBar = kP + kDcMat;
+    static constexpr int kB = kV + 16384;       // workspace blocks up to P': 2 stages
+    static constexpr int kP = kB + 2 * kDcHead; // P' hi, P' lo
+    // outputs: a tile of [kTok tokens x 32 values] per compute warp, with two CTAs an SM in the
+    // place of the q chunk, which has been read by then
+    static constexpr int kY = DwShape<G>::kLate ? kP + 2 * kDcMat : kQ;
+    static constexpr int kBar = kP + 2 * kDcMat + (DwShape<G>::kLate ? 16384 : 0);
     static constexpr int kTmem = kBar + 144;
     static constexpr int kAlive = kTmem + 4;  // the walk for M: chunks after which it was not 0
     static constexpr int kDone = kAlive + 4;  // and whether it has become 0
@@ -602,7 +625,7 @@ struct DwSmem { // from a 1024-byte aligned base
     static constexpr int kBytes = kBar + 256;
 };
 // two CTAs on an SM: 228 KB, 1 KB of it reserved for each
-static_assert(DwSmem::kBytes <= 113 * 1024, "shared memory of the walk");
+static_assert(DwSmem<2>::kBytes <= 113 * 1024 && DwSmem<4>::kBytes <= 227 * 1024, "shared memory of the walk");
 
 struct DeltaWalkArgs {
     DeltaArgs d; // as called: for the columns that are walked token by token
@@ -849,19 +872,20 @@ __global__ void __launch_bounds__(DwShape<G>::kThreads, DwShape<G>::kCtas)
 ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_constant__ DeltaWalkMaps maps, uint32_t *status)
 {
     using Sh = DwShape<G>;
+    using Sm = DwSmem<G>;
     constexpr int kWarps = Sh::kWarps, kTok = Sh::kTok, kKeys = Sh::kKeys;
     constexpr bool kLate = Sh::kLate;
     extern __shared__ __align__(1024) unsigned char dw_sm[];
     unsigned char *sm = dw_sm;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + DwSmem::kBar);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sm::kBar);
     // loads (k, workspace block: two stages each), products, and the compute warps' arrivals
     uint64_t *bar_k = bars, *bar_b = bars + 2, *bar_q = bars + 4, *bar_v = bars + 5, *bar_p = bars + 6,
              *bar_kh = bars + 7, *bar_u = bars + 8, *bar_qh = bars + 9, *bar_y = bars + 10, *bar_dh = bars + 11 /* [2] */;
     uint64_t *arr_h = bars + 13, *arr_q = bars + 14, *arr_r = bars + 15, *arr_u = bars + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + DwSmem::kTmem);
-    volatile int *s_alive = reinterpret_cast<int *>(sm + DwSmem::kAlive);
-    volatile int *s_done = reinterpret_cast<int *>(sm + DwSmem::kDone);
-    volatile int *s_bad = reinterpret_cast<int *>(sm + DwSmem::kBad);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Sm::kTmem);
+    volatile int *s_alive = reinterpret_cast<int *>(sm + Sm::kAlive);
+    volatile int *s_done = reinterpret_cast<int *>(sm + Sm::kDone);
+    volatile int *s_bad = reinterpret_cast<int *>(sm + Sm::kBad);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const bool issuer = warp == kWarps;
@@ -934,27 +958,27 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 begin(bar_k + st);
                 begin(bar_b + st);
                 mbar_arrive_expect_tx(bar_k + st, 16384);
-                tma_load_4d(sm + DwSmem::kK + st * 16384, &maps.k, 0, hk, t, b32, bar_k + st);
-                tma_load_4d(sm + DwSmem::kK + st * 16384 + 8192, &maps.k, 64, hk, t, b32, bar_k + st);
+                tma_load_4d(sm + Sm::kK + st * 16384, &maps.k, 0, hk, t, b32, bar_k + st);
+                tma_load_4d(sm + Sm::kK + st * 16384 + 8192, &maps.k, 64, hk, t, b32, bar_k + st);
                 mbar_arrive_expect_tx(bar_b + st, kDcHead);
-                bulk_load(sm + DwSmem::kB + st * kDcHead, blocks + int64_t(c) * kDcBlockBytes, kDcHead, bar_b + st);
+                bulk_load(sm + Sm::kB + st * kDcHead, blocks + int64_t(c) * kDcBlockBytes, kDcHead, bar_b + st);
             };
             auto load_p = [&](int c) {
                 begin(bar_p);
-                mbar_arrive_expect_tx(bar_p, kDcMat);
-                bulk_load(sm + DwSmem::kP, blocks + int64_t(c) * kDcBlockBytes + kDcP, kDcMat, bar_p);
+                mbar_arrive_expect_tx(bar_p, 2 * kDcMat);
+                bulk_load(sm + Sm::kP, blocks + int64_t(c) * kDcBlockBytes + kDcP, 2 * kDcMat, bar_p);
             };
             auto load_q = [&](int c) {
                 begin(bar_q);
                 mbar_arrive_expect_tx(bar_q, 16384);
-                tma_load_4d(sm + DwSmem::kQ, &maps.q, 0, hk, t_first + c * kDcChunk, b32, bar_q);
-                tma_load_4d(sm + DwSmem::kQ + 8192, &maps.q, 64, hk, t_first + c * kDcChunk, b32, bar_q);
+                tma_load_4d(sm + Sm::kQ, &maps.q, 0, hk, t_first + c * kDcChunk, b32, bar_q);
+                tma_load_4d(sm + Sm::kQ + 8192, &maps.q, 64, hk, t_first + c * kDcChunk, b32, bar_q);
             };
             auto load_v = [&](int c) {
                 begin(bar_v);
                 mbar_arrive_expect_tx(bar_v, 16384);
-                tma_load_4d(sm + DwSmem::kV, &maps.v, n0, h, t_first + c * kDcChunk, b32, bar_v);
-                tma_load_4d(sm + DwSmem::kV + 8192, &maps.v, n0 + 64, h, t_first + c * kDcChunk, b32, bar_v);
+                tma_load_4d(sm + Sm::kV, &maps.v, n0, h, t_first + c * kDcChunk, b32, bar_v);
+                tma_load_4d(sm + Sm::kV + 8192, &maps.v, n0 + 64, h, t_first + c * kDcChunk, b32, bar_v);
             };
             constexpr uint32_t kIdTok = idesc_bf16(128, kDcChunk, 0, 0), kIdHalf = idesc_bf16(128, 32, 0, 0);
             // dH in halves of 64 keys
@@ -969,29 +993,36 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
             }
             if (nc > 1)
                 load_kb(1);
-            // H^T Q^T into Y^T
-            auto mul_qh = [&](uint32_t dy) {
-                for (int ks = 0; ks < a.nks; ++ks)
-                    umma_bf16_ts(dy, tmem + kDwH + 16 * ks,
-                                 sw128_desc(s_base + DwSmem::kQ + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), kIdTok,
-                                 ks > 0);
+            // H^T Q^T into Y^T; rest: with the remainders of H
+            auto mul_qh = [&](uint32_t dy, bool rest) {
+                for (int ks = 0; ks < a.nks; ++ks) {
+                    const uint64_t qd = sw128_desc(s_base + Sm::kQ + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024);
+                    umma_bf16_ts(dy, tmem + kDwH + 16 * ks, qd, kIdTok, ks > 0);
+                    if (rest)
+                        umma_bf16_ts(dy, tmem + kDwH + 16 * ks + 8, qd, kIdTok, 1);
+                }
                 commit(bar_qh);
             };
-            // + U^T P^T, in halves of another shape: after H^T Q^T has completed
-            auto mul_up = [&](uint32_t dy) {
+            // + (w o U)^T P'^T, or U^T P'^T, in halves of another shape: after H^T Q^T has completed
+            auto mul_up = [&](uint32_t dy, bool copy) {
+                const uint32_t uh = tmem + (copy ? Sh::kUh : kDwD2), ul = tmem + (copy ? Sh::kUl : kDwD2 + 8);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                    for (int ks = 0; ks < 2 + 2 * hf; ++ks)
-                        umma_bf16_ts(dy + 32 * hf, tmem + Sh::kU + 16 * ks,
-                                     sw32_desc(s_base + DwSmem::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0)), kIdHalf, 1);
+                    for (int ks = 0; ks < 2 + 2 * hf; ++ks) {
+                        const uint32_t at = s_base + Sm::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0);
+                        const uint64_t ph = sw32_desc(at), pl = sw32_desc(at + kDcMat);
+                        umma_bf16_ts(dy + 32 * hf, uh + 16 * ks, ph, kIdHalf, 1);
+                        umma_bf16_ts(dy + 32 * hf, ul + 16 * ks, ph, kIdHalf, 1);
+                        umma_bf16_ts(dy + 32 * hf, uh + 16 * ks, pl, kIdHalf, 1);
+                    }
                 commit(bar_y);
             };
             for (int c = 0; c < nc; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
                 const uint32_t d1 = tmem + kDwD1, dy = tmem + Sh::kY + (c & 1) * Sh::kYStep;
-                const uint32_t kb = s_base + DwSmem::kK + st * 16384, bb = s_base + DwSmem::kB + st * kDcHead;
+                const uint32_t kb = s_base + Sm::kK + st * 16384, bb = s_base + Sm::kB + st * kDcHead;
                 // KH^T once the tile has landed and H(c) is written
                 if (!mbar_wait(bar_k + st, ph2, status) || !mbar_wait(arr_h, ph, status)) {
                     ok = false;
@@ -1017,6 +1048,8 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     load_p(c);
+                    if (!kLate) // the outputs of c - 1 have left its place (before H(c) was written)
+                        load_q(c);
                 }
                 if (outs && kLate) {
                     if (!mbar_wait(bar_q, ph, status) || !mbar_wait(arr_q, ph, status)) {
@@ -1024,7 +1057,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_qh(dy);
+                    mul_qh(dy, true);
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
                 if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
@@ -1032,6 +1065,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                     break;
                 }
                 tc_fence_after();
+                const bool copy = reinterpret_cast<const volatile float *>(sm + Sm::kB + st * kDcHead + kDcE)[1] != 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -1066,10 +1100,10 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_qh(dy);
+                    mul_qh(dy, !copy); // (the remainders' places may be taken by U)
                 }
-                // U is written: dH^T over H, which has been read (with two CTAs its first half
-                // while U^T P^T completes, whose U lies in the place of the second)
+                // U is written: dH^T over H, which has been read (with two CTAs a copy of U, in the
+                // place of H's remainders, too)
                 if (!mbar_wait(arr_u, ph, status) || (outs && !mbar_wait(bar_p, ph, status))) {
                     ok = false;
                     break;
@@ -1081,7 +1115,12 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_up(dy);
+                    mul_up(dy, copy);
+                    if (copy && !mbar_wait(bar_y, ph, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                 }
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
@@ -1091,11 +1130,6 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 }
                 commit(bar_dh);
                 if (a.nks > 4) {
-                    if (outs && !kLate && !mbar_wait(bar_y, ph, status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t kd = sw128_desc(kb + 8192 + ks * 2048, 8192, 1024);
@@ -1105,9 +1139,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 }
                 commit(bar_dh + 1);
                 if (outs && kLate)
-                    mul_up(dy);
-                if (c + 1 < nc && outs && !kLate)
-                    load_q(c + 1);
+                    mul_up(dy, copy);
             }
             // let every load and product in flight finish before the tensor memory is freed:
             // the latest phase of each barrier
@@ -1181,8 +1213,8 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 store_h(m, kb);
         tmem_st_wait();
         arrive(arr_h);
-        const uint32_t v_base = s_base + DwSmem::kV + (row0 >> 6) * 8192; // the tile of this warp's values
-        unsigned char *ytile = sm + DwSmem::kY + warp * (64 * kTok);
+        const uint32_t v_base = s_base + Sm::kV + (row0 >> 6) * 8192; // the tile of this warp's values
+        unsigned char *ytile = sm + Sm::kY + warp * (64 * kTok);
         const uint32_t y_base = smem_u32(ytile);
         // this lane's 16 bytes of the tile's first eight rows; eight rows further on, ystep more
         const int64_t ystep = int64_t(8) * a.heads_v * a.dv;
@@ -1191,7 +1223,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
         for (int c = 0; c < nc; ++c) {
             const int st = c & 1;
             const uint32_t ph = uint32_t(c & 1), ph2 = uint32_t((c >> 1) & 1);
-            const unsigned char *blk = sm + DwSmem::kB + st * kDcHead;
+            const unsigned char *blk = sm + Sm::kB + st * kDcHead;
             const float *sc = reinterpret_cast<const float *>(blk + kDcC) + kTok * cg + tc;
             const float *sw = reinterpret_cast<const float *>(blk + kDcW) + kTok * cg + tc;
             const float *ss_ = reinterpret_cast<const float *>(blk + kDcS);
@@ -1204,17 +1236,15 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 break;
             }
             const float2 em = *reinterpret_cast<const float2 *>(blk + kDcE); // E_63, mode
-            // ---- s o Q in place (bf16), in chunks whose decays leave the range of P' ---------
-            if (outs && em.y != 0.0f) {
-                if (!wait(bar_q, ph)) {
-                    ok = false;
-                    break;
-                }
+            // ---- 2^e o Q in place, in chunks with cuts or strong decays; with two CTAs while U^T runs
+            auto scale_q = [&]() {
+                if (!wait(bar_q, ph))
+                    return false;
 #pragma unroll 1
                 for (int i = 0; i < 1024 / (32 * kWarps); ++i) {
                     const int e = tid + 32 * kWarps * i; // 16-byte chunk: tile, token, position
-                    const float s = ss_[(e >> 3) & 63];
-                    uint4 *p = reinterpret_cast<uint4 *>(sm + DwSmem::kQ + 16 * e);
+                    const float s = dc_power(ss_[(e >> 3) & 63]);
+                    uint4 *p = reinterpret_cast<uint4 *>(sm + Sm::kQ + 16 * e);
                     const uint4 v = *p;
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                     uint32_t o[4];
@@ -1224,8 +1254,14 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                     *p = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 fence_proxy_async_smem();
+                return true;
+            };
+            if (kLate && outs && em.y != 0.0f && !scale_q()) {
+                ok = false;
+                break;
             }
-            arrive(arr_q);
+            if (kLate)
+                arrive(arr_q);
             // ---- R^T = V^T - KH^T diag(c) -------------------------------------------------
             if ((!for_m && !wait(bar_v, ph)) || !wait(bar_kh, ph)) {
                 ok = false;
@@ -1263,7 +1299,13 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
             tmem_st_wait();
             if (!(a.hold && c == 0))
                 arrive(arr_r);
-            // ---- U^T rounded, and w o U over it -----------------------------------------------
+            if (!kLate && outs && em.y != 0.0f && !scale_q()) {
+                ok = false;
+                break;
+            }
+            if (!kLate)
+                arrive(arr_q);
+            // ---- w o U over U^T, and where the outputs need it a copy of U^T ---------------------
             if (!wait(bar_u, ph)) {
                 ok = false;
                 break;
@@ -1273,20 +1315,23 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + kTok * cg;
 #pragma unroll
                 for (int j = 0; j < kTok / 16; ++j) {
-                    uint32_t r[8], w[8], u[4];
+                    uint32_t r[8], w[8];
                     tmem_ld_frag(at + 16 * j, r);
+                    if (outs && em.y != 0.0f) {
+                        uint32_t uh[4], ul[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dw_split2(dw_pair(r, i), uh[i], ul[i]);
+                        tmem_st_frag(ml + Sh::kUh + 16 * (kTok / 16 * cg + j), uh);
+                        tmem_st_frag(ml + Sh::kUl + 16 * (kTok / 16 * cg + j), ul);
+                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float2 wv = *reinterpret_cast<const float2 *>(sw + 16 * j + 8 * i);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float2 uu = dw_pair(r, 2 * i + x);
-                            u[2 * i + x] = pack_bf16x2(uu.x, uu.y);
-                            dw_split2(__fmul2_rn(wv, uu), w[2 * i + x], w[4 + 2 * i + x]);
-                        }
+                        for (int x = 0; x < 2; ++x)
+                            dw_split2(__fmul2_rn(wv, dw_pair(r, 2 * i + x)), w[2 * i + x], w[4 + 2 * i + x]);
                     }
-                    if (outs)
-                        tmem_st_frag(ml + Sh::kU + 16 * (kTok / 16 * cg + j), u);
                     tmem_st_frag(at + 16 * j, w);
                 }
             }
@@ -1305,8 +1350,8 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float2 sv = *reinterpret_cast<const float2 *>(ss_ + kTok * cg + 16 * j + 8 * i + tc);
-                            sv.x = em.y == 0.0f ? sv.x : 1.0f;
-                            sv.y = em.y == 0.0f ? sv.y : 1.0f;
+                            sv.x = em.y == 0.0f ? sv.x : dc_mantissa(sv.x);
+                            sv.y = em.y == 0.0f ? sv.y : dc_mantissa(sv.y);
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * i + x));
@@ -1335,6 +1380,8 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                             *reinterpret_cast<uint4 *>(yp + i * ystep) = *reinterpret_cast<const uint4 *>(src + 512 * i);
                     yp += (kDcChunk / 8) * ystep;
                 }
+                if (!kLate) // the next q chunk may land in the tiles' place
+                    fence_proxy_async_smem();
             };
             if (outs && !kLate) {
                 if (!wait(bar_y, ph)) {

@@ -165,15 +165,14 @@ def test_error_of_the_chunked_form_in_norm(orc, shape, slow):
     mantissa); keeping the remainder in bfloat16 too leaves the square of it, 2.8e-6.  The
     state: five such splits on the way of a chunk (H, R, T, w o U and the product of two
     remainders that is left out), 6.2e-6 as they fall, tripled for the chunks that a state
-    remembers.  The outputs: the rounding of their own and of H in Q H, and of P and U in P U,
-    where the terms of a sum may be half as large again as the sum in norm:
-    1.66e-3 sqrt(1 + 1 + 2 x 1.5^2) = 4.2e-3.  A lost remainder would cost the state 1e-3."""
+    remembers.  The outputs: the rounding of their own, and in chunks with a cut or strong
+    decays that of H in Q H: 1.66e-3 sqrt(2) = 2.4e-3.  A lost remainder would cost either 1e-3."""
     inp = make_delta_inputs(*shape, "bf16", seed=3660 + sum(shape), h0=True)
     if slow:
         inp["g"] = inp["g"] * 1e-2
     y, fs = _scan(inp, scale=1.0, qk_l2norm=True)
     ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
-    for got, want, tol, what in ((y, ref["outputs"], 4.2e-3, "outputs"), (fs, ref["final_state"], 1.9e-5, "state")):
+    for got, want, tol, what in ((y, ref["outputs"], 2.4e-3, "outputs"), (fs, ref["final_state"], 1.9e-5, "state")):
         want = torch.from_numpy(want)
         err = float((got.double() - want).norm() / want.norm())
         assert err <= tol, f"{what}: {err:.2e}"
@@ -200,4 +199,32 @@ def _check_forms(orc, inp, workspace, scale):
     y, fs = _scan(inp, scale=scale, qk_l2norm=True, workspace=workspace)
     ref = orc.delta_scan(**inp, scale=scale, qk_l2norm=True)
     assert_close(y, ref["outputs"], TOL[y.dtype], "outputs")
+    assert_close(fs, ref["final_state"], TOL[F32], "final state")
+
+
+@pytest.mark.parametrize("heads_v,seq", [(2, 500), (150, 200), (2, 2400)])
+@pytest.mark.parametrize("decay", ["none", "slow", "strong", "resets"])
+@pytest.mark.parametrize("spread", [0.0, 0.1, 1.0])
+@pytest.mark.parametrize("same", [True, False])
+def test_keys_that_resemble_each_other(orc, heads_v, seq, decay, spread, same):
+    """Keys around one direction (spread: their own part to the common one), read with
+    themselves or with other queries: every write replaces most of the one before, and the
+    terms of an output add up to a multiple of it.  The tolerances are the framework's, and in
+    norm that of any other outputs (see above)."""
+    inp = make_delta_inputs(1, seq, 1, heads_v, 128, 64, "bf16", seed=3680, h0=True)
+    gen = torch.Generator().manual_seed(3681)
+    k = torch.randn(1, 1, 1, 128, generator=gen) + spread * torch.randn(1, seq, 1, 128, generator=gen)
+    inp["k"] = k.to(BF16)
+    inp["q"] = inp["k"] if same else torch.randn(1, seq, 1, 128, generator=gen).to(BF16)
+    inp["v"] = torch.randn(1, seq, heads_v, 64, generator=gen).to(BF16)
+    inp["g"] = torch.full_like(inp["g"], {"none": 0.0, "slow": -0.03, "strong": -1.0, "resets": -0.03}[decay])
+    inp["beta"] = 0.5 + 0.5 * torch.rand(inp["beta"].shape, generator=gen)
+    inp["beta"][..., 0] = 1.0
+    if decay == "resets":
+        inp["reset"] = torch.rand(1, seq, generator=gen) < 0.02
+    y, fs = _scan(inp, scale=1.0, qk_l2norm=True)
+    ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
+    assert_close(y, ref["outputs"], TOL[BF16], "outputs")
+    want = torch.from_numpy(ref["outputs"])
+    assert float((y.double() - want).norm() / want.norm()) <= 2.4e-3
     assert_close(fs, ref["final_state"], TOL[F32], "final state")

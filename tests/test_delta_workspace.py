@@ -9,7 +9,7 @@ from selective_state_space_18_b200 import build as ssbuild
 from selective_state_space_18_b200 import ssscan
 from selective_state_space_18_b200.inputs import make_delta_inputs
 
-BLOCK = 3 * 6144 + 4 * 256  # T in two parts, P, and four arrays of 64 floats, per chunk and head
+BLOCK = 4 * 6144 + 4 * 256  # T and P in two parts each, and four arrays of 64 floats, per chunk and head
 P = [0x7f0000000000 + i * 0x100000000 for i in range(12)]
 
 
