@@ -211,7 +211,7 @@ SS_API int ss_scan_status(const void *workspace, ss_stream_t stream, int *status
 
 /*
  * The device status word of calls made without a workspace (ss_scan_fwd with a NULL
- * workspace, and every decode call) on the current device: ss_scan_status(NULL,
+ * workspace, and every decode call), and of ss_delta_scan, on the current device: ss_scan_status(NULL,
  * stream, ...) as one return value.  Synchronises `stream`, reads and clears the word,
  * and returns SS_OK, SS_ERR_TIMEOUT (a bounded device-side wait gave up; those calls'
  * outputs are invalid) or the error status of the query itself.
@@ -395,18 +395,20 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *   v           : [batch, seq, heads_v, dv] dtype   and v_stride elements apart (at least
  *                 the heads' width; batch rows seq * stride apart), so that all three may
  *                 be slices of one projection's output
- *   g           : [batch, seq, heads_v] float32, nullable (no decay): log decays, any
- *                 value below +infinity; -infinity discards the state
+ *   g           : [batch, seq, heads_v] float32, nullable (no decay): log decays up to
+ *                 88.7 (e^g is a float32 number); -infinity discards the state
  *   beta        : [batch, seq, heads_v] float32, nullable (1), any value
  *   reset       : [batch, seq] uint8, nullable
  *   h0          : [batch, heads_v, dk, dv] float32, nullable
  *   flags       : SS_QK_L2NORM: q and k stand for q / sqrt(|q|^2 + 1e-6) and the same of k
+ *                 (the sums of squares are float32: elements up to about 1e18)
  *   outputs     : [batch, seq, heads_v, dv] dtype
  *   final_state : [batch, heads_v, dk, dv] float32, nullable; may be h0 itself
  *   workspace   : device buffer of at least ss_delta_workspace_bytes() bytes, 16-byte
  *                 aligned, or NULL.  Its contents need no preparation and mean nothing
- *                 between calls; calls that share it must be ordered.  Without it (or for
- *                 shapes that need none) the token-by-token kernel runs.
+ *                 between calls; calls that share it must be ordered (captured graphs
+ *                 that share one, too).  Without it (or for shapes that need none) the
+ *                 token-by-token kernel runs.
  *
  * heads_v must be a multiple of heads_k (SS_ERR_SHAPE), dk at most 256
  * (SS_ERR_UNSUPPORTED).  An infinity or NaN among the inputs reaches the results that
@@ -417,13 +419,16 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *    16-byte aligned tensors, strides that are multiples of 8 and a workspace: chunks of 64
  *    tokens on the tensor cores.  The state is held in float32 and computed operands in 16
  *    bits of mantissa: final_state follows float32 arithmetic to about 5e-6 of its size (to
- *    4e-5 with keys that resemble each other, to 1e-3 where beta |k|^2 nears 2 as well), and
- *    outputs are off by little more than their own rounding.  Few heads and a long sequence
+ *    4e-5 with keys that resemble each other or beta |k|^2 past 1, to 1e-3 with both where
+ *    nothing decays), and outputs are off by little more than their own rounding.  Few heads and a long sequence
  *    are cut into segments that run at once.  Columns whose state or outputs become infinite
  *    or NaN on the way (writes past about 1e20 under strong decays do, too) are walked once
  *    more token by token, 2.6 us each: right, but not fast;
- *  - every other case: token by token, all arithmetic in float32.
- * Results are the same from call to call.
+ *  - every other case: token by token, all arithmetic in float32.  A long prompt takes
+ *    many times as long (16384 tokens x 32 heads in bf16: 5.3 ms for dk = dv = 100, 0.54 ms
+ *    for 104), so sizes, strides and addresses outside the first form are worth padding.
+ * Results are the same from call to call.  A device-side wait that gave up is reported by
+ * ss_debug_status, with a workspace too (ss_scan_status does not take this one).
  */
 enum { SS_QK_L2NORM = 4u };
 SS_API int ss_delta_scan(int64_t batch, int64_t seq, int64_t heads_k, int64_t heads_v, int64_t dk, int64_t dv,
@@ -468,7 +473,8 @@ SS_API int ss_delta_update(int64_t batch, int64_t heads_k, int64_t heads_v, int6
  *                  each nullable (1, 0)
  *   y            : [rows, groups * size] dtype (output, contiguous)
  *
- * size at most SS_GROUP_NORM_MAX_SIZE and eps >= 0 (SS_ERR_UNSUPPORTED otherwise).
+ * size at most SS_GROUP_NORM_MAX_SIZE and eps >= 0 (SS_ERR_UNSUPPORTED otherwise).  Sums are
+ * float32: x' up to about 1e17 in size.
  */
 #define SS_GROUP_NORM_MAX_SIZE 16384
 enum { SS_NORM_CENTER = 1u, SS_NORM_GATE_FIRST = 2u, SS_NORM_SILU = 4u, SS_NORM_SHARED = 8u };

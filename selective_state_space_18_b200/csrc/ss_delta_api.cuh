@@ -83,19 +83,27 @@ template <typename T> int dispatch_delta_rec(const ss::DeltaArgs &a, cudaStream_
 
 // Shapes the chunked form takes (bf16; q, k and v as rows of whole 16-byte vectors, which
 // TMA asks for; keys of 8 would leave seven eighths of the tiles empty).  Prompts of up to
-// 16 tokens are walked token by token: 8.3 us for 16 heads x 16 tokens, where the two
-// launches of the chunked form take 15.5 us for one chunk of 32 heads.
+// 16 tokens are walked token by token.  The state then keeps float32's accuracy where a prompt
+// comes in many small pieces (the chunked form costs it 5e-6 a call), and with few heads it is
+// the faster form, too: 16 heads x 16 tokens 14 us against 22 us, 32 heads 22 us in either.
+// With many heads it is the slower one at any length: 256 heads x 16 tokens 113 us against
+// 31 us, 2048 heads 782 us against 137 us.
 bool delta_chunked_shape(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_dtype_t dtype)
 {
     return dtype == SS_BF16 && dk >= 16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 && seq > 16 && seq < (int64_t(1) << 31) - 64 &&
            batch < (int64_t(1) << 31);
 }
 
-// Segments of the two-pass walk (1: one pass).  Two passes over 1/S of the chunks, with
-// most SMs holding two walks (1.4 times as long a step each), and the join, against one
-// pass: measured on 256 chunks x 32 heads, 0.94 ms in one pass, 0.61, 0.62 and 0.54 ms with 4,
-// 5 and 6 segments (an earlier walk: 0.62, 0.55, 0.55, 0.56 and 0.59 ms with 4, 6, 7, 9 and
-// 12), and nothing gained on 24 chunks x 36 heads (97 to 116 us with 4 to 6, 99 us in one).
+// Segments of the two-pass walk (1: one pass): as many as make 192 walks in pass 2, each of 12
+// chunks or more.  Two passes and the join against one pass, heads of 128 x 128, in us:
+//   heads            1          8         16         32         48         64
+//   36 chunks   98 / 123  102 / 127  107 / 131  121 / 141  135 / 152  186 / 162
+//   64 chunks  115 / 207  121 / 213  131 / 223  197 / 238  234 / 254  291 / 268
+//   256 chunks 188 / 766  262 / 817  362 / 846  537 / 893  756 / 944  983 / 1002
+// (64 heads of 36 to 64 chunks are on the wrong side by up to 15%.)  With 148 walks, one an SM:
+// 573 us for 256 chunks x 32 heads, but 242, 317 and 694 us with 8, 16 and 48 heads.  Segments
+// of 8 chunks and more: 88 us for 36 chunks of one head, but 217 us for 256, whose join is
+// longer; of 16 and more: 131 us for 256 chunks of one head, none for 36.
 constexpr int64_t kDeltaWalks = 192; // of pass 2
 int64_t delta_segments(int64_t heads, int64_t tiles, int64_t chunks)
 {

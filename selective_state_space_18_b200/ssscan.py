@@ -241,8 +241,8 @@ def ss_scan_status(workspace=None, stream=None, device=None):
 
 
 def ss_debug_status(stream=None, device=None):
-    """Read and clear the device status word of the calls made without a workspace on
-    `device` (synchronises the stream): 'SS_OK' or 'SS_ERR_TIMEOUT'."""
+    """Read and clear the device status word of the calls made without a workspace, and of
+    ss_delta_scan, on `device` (synchronises the stream): 'SS_OK' or 'SS_ERR_TIMEOUT'."""
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
@@ -774,7 +774,11 @@ def ss_delta_scan(q, k, v, g=None, beta=None, *, reset=None, h0=None, scale=None
     q, "final_state": [batch, heads_v, dk, dv] float32 (None when not returned)}.
 
     workspace: True (allocated for the call), False (none: the token-by-token kernel) or a
-    uint8 tensor of ss_delta_workspace_bytes() bytes; ``final_state`` may be h0 itself.
+    uint8 tensor of ss_delta_workspace_bytes() bytes, which calls that are not ordered (two
+    streams, two captured graphs) must not share; ``final_state`` may be h0 itself.
+    bfloat16 with dk a multiple of 8 from 16 to 128, dv a multiple of 8, more than 16 tokens
+    and rows of whole 16 bytes runs in chunks on the tensor cores; everything else token by
+    token, ten times slower on long prompts.  g is at most 88.7 (e^g is a float32 number).
     An infinity or NaN reaches the results that depend on it and no others."""
     index, dt = q.get_device(), q.dtype
     if stream is not None or index < 0 or index != torch.cuda.current_device():
