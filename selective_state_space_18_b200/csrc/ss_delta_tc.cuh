@@ -28,10 +28,10 @@
 //   Y^T  [128 x 64]  = (H^T Q^T + (w o U)^T P'^T) diag(s),   P'_ij = q_i.k_j / E_63  (j <= i)
 //   dH^T [128 x dk]  = (w o U)^T K          H = E_63 H + dH
 // since P_ij = s_i P'_ij w_j without a cut in the chunk.  One operand serves both products.
-// P' and w are only in range where the chunk's decays are: with a cut in the chunk, or decays
-// beyond 2^-60 in all, U^T is kept beside w o U, P' is P_ij / m_i, and the walk scales the rows
-// of Q by 2^e_i in shared memory, for s_i = m_i 2^e_i: exactly, with m_i left for the end (the
-// block says which).
+// P' and w are only in range where the chunk's decays are.  With a cut in the chunk, or decays
+// beyond 2^-60 in all, s and w are taken apart into powers of two and the rest, from 1 to 2:
+// the walk scales the rows of Q and K by the powers in shared memory, which rounds nothing, the
+// rest takes the place of s and w, and P'_ij is P_ij over both (the block says which).
 //
 // Few heads and a long prompt leave most SMs without a walk.  The sequence is then cut into
 // segments that are walked at once, in two passes ("s6_reset" blog draft, Associative
@@ -45,11 +45,10 @@
 // Precision.  q, k and v are bf16 inputs and enter exactly.  On the way from state to
 // state the computed operands (H, R, T, w o U) are split, x = hi + lo to 2^-17, and their
 // products summed in fp32, so the final state follows fp32 arithmetic to about 5e-6 of
-// its size.  So do those on the way to the outputs (H, w o U or U, P'): where keys resemble each
+// its size.  So do those on the way to the outputs (H, w o U, P'): where keys resemble each
 // other the terms of P U are many times its sum, and operands of 8 bits were off by up to 0.13
-// in outputs of order one.  Only in chunks with a cut or strong decays does H enter H^T Q^T
-// rounded to bf16 (two walks an SM: its remainder has made room for U^T).  Output error 1.7e-3
-// of the norm, which is the rounding of the output itself, and up to 2.4e-3 in such chunks.
+// in outputs of order one.  Output error 1.7e-3 of the norm, which is the rounding of the output
+// itself.
 //
 // Decays.  The cumulative log2 decays are kept as a part of multiples of 1/64, which sums
 // and differences exactly, and a remainder below 1/128 a token, each with an exponential of its
@@ -74,8 +73,9 @@ namespace ss {
 constexpr int kDcChunk = 64; // tokens per chunk
 constexpr float kDcLog2eRest = float(1.4426950408889634 - double(kLog2e)); // log2(e) beyond kLog2e
 
-// A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63 and the mode: 0, or 1 for
-// cuts and strong decays), then P' hi, P' lo.  A matrix is
+// A block: T hi, T lo, four arrays of 64 floats (c, w, s; then E_63, the mode: 0, or 1 for cuts
+// and strong decays, and from kDcPow on the powers of two of w and of s as the exponents' eight
+// bits), then P' hi, P' lo.  A matrix is
 // four slices ks of 32-byte rows in the 32-byte swizzle: columns 16 ks .. 16 ks + 15, rows
 // 0..63 of the first two slices and 32..63 of the last two (the rest is above the diagonal
 // and 0).  Products with it accumulate into two halves of 32 tokens each, always with
@@ -87,11 +87,12 @@ constexpr int kDcThi = 0, kDcTlo = kDcMat, kDcC = 2 * kDcMat, kDcW = kDcC + 256,
               kDcP = kDcE + 256;
 constexpr int kDcHead = kDcP;                     // the part loaded ahead of P
 constexpr int kDcBlockBytes = kDcP + 2 * kDcMat;  // workspace per chunk and value head
+constexpr int kDcPow = kDcE + 16;
 static_assert(kDcHead % 1024 == 0 && kDcBlockBytes == 25600, "workspace block");
 
-// s = m 2^e: the power of two (0 for 0 and below float32's normal range) and m (1 to 2 in
-// size, with the sign), whose product is s, or 0 there.
-__device__ __forceinline__ float dc_power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7f800000u); }
+// x = m 2^e: the bits of the power of two (0 for 0 and below float32's normal range) and m (1 to
+// 2 in size, with the sign), whose product is x, or 0 there.
+__device__ __forceinline__ unsigned char dc_power(float x) { return (unsigned char)(__float_as_uint(x) >> 23); }
 __device__ __forceinline__ float dc_mantissa(float s)
 {
     return __uint_as_float((__float_as_uint(s) & 0x807fffffu) | 0x3f800000u);
@@ -375,15 +376,21 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
         const float r = sR[tid];
         reinterpret_cast<float *>(blk + kDcC)[tid] = r * e;
         // the decays factor through the chunk's start where E is in range
-        sF[tid] = r * (ex2(-gh) * ex2(-gl));
+        sF[tid] = r * (ex2(-gh) * ex2(-gl)); // (1 / w where it is not)
         sB[tid] = be * r * e;
         const bool hand = sRed[3] != 0.0f; // the next chunk's first token does not cut
-        const float se = sP[tid] * e;
+        float se = sP[tid] * e;
+        float we = hand && cut == sN[63] ? r * (ex2(sGh[63] - gh) * ex2(sGl[63] - gl)) : 0.0f;
+        if (direct) {
+            blk[kDcPow + tid] = dc_power(we);
+            blk[kDcPow + 64 + tid] = dc_power(se);
+            we = dc_mantissa(we);
+            se = dc_mantissa(se);
+            sF[tid] = 1.0f / we;
+            sP[tid] = sP[tid] / se;
+        }
+        reinterpret_cast<float *>(blk + kDcW)[tid] = we;
         reinterpret_cast<float *>(blk + kDcS)[tid] = se;
-        if (direct)
-            sP[tid] = sP[tid] / dc_mantissa(se);
-        reinterpret_cast<float *>(blk + kDcW)[tid] =
-            hand && cut == sN[63] ? r * (ex2(sGh[63] - gh) * ex2(sGl[63] - gl)) : 0.0f;
         if (tid == 0) {
             reinterpret_cast<float *>(blk + kDcE)[0] = !hand || sN[63] ? 0.0f : ex2(sGh[63]) * ex2(sGl[63]);
             reinterpret_cast<float *>(blk + kDcE)[1] = direct ? 1.0f : 0.0f;
@@ -411,8 +418,10 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
                             float2 av = __fmul2_rn(__fmul2_rn(f, make_float2(b1, b1)),
                                                    make_float2(kk[nt][2 * x], kk[nt][2 * x + 1]));
                             const float2 pf = make_float2(p1, p1);
-                            float2 pv = __fmul2_rn(both ? __fmul2_rn(f, pf) : pf,
-                                                   make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]));
+                            float2 pv = make_float2(qk[nt][2 * x], qk[nt][2 * x + 1]);
+                            pv = __fmul2_rn(both ? __fmul2_rn(__fmul2_rn(f, *reinterpret_cast<const float2 *>(sF + j)), pf)
+                                                 : pf,
+                                            pv);
                             if (jb >= warp) { // on or above the diagonal blocks
                                 av.x = j < i ? av.x : 0.0f;
                                 av.y = j + 1 < i ? av.y : 0.0f;
@@ -597,15 +606,11 @@ template <int G> struct DwShape {
     static constexpr uint32_t kCols = kLate ? 512 : 256; // tensor memory
     static constexpr uint32_t kY = kLate ? 256 : 128;    // Y^T
     static constexpr uint32_t kYStep = kLate ? 64 : 0;   // from Y^T of even chunks to that of odd ones
-    // U^T for Y in chunks with cuts or strong decays, high parts and remainders: 8 columns of
-    // 16 tokens, 16 columns apart
-    static constexpr uint32_t kUh = kLate ? 384 : 72, kUl = kLate ? 392 : 8;
 };
 // tensor-memory columns.  H: 16 columns per 16 keys, the high parts of H^T in the first
 // 8 (packed pairs), the remainders in the last 8; dH^T is accumulated over them.  D1: KH^T,
 // then R^T over it in the same form (16 columns per 16 tokens).  D2: U^T, then
-// (w o U)^T over it.  U^T lies in the places of remainders of H that KH^T has read, or has its
-// own where there is room.
+// (w o U)^T over it.
 constexpr uint32_t kDwH = 0, kDwD1 = 128, kDwD2 = 192;
 
 template <int G> struct DwSmem { // from a 1024-byte aligned base
@@ -678,6 +683,14 @@ __device__ __forceinline__ void dw_split2(float2 x, uint32_t &hi, uint32_t &lo)
     lo = pack_bf16x2(r.x, r.y);
 }
 
+// (exact for a power of two)
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ float2 dw_pair(const uint32_t (&r)[8], int e)
 {
     return make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
@@ -714,12 +727,6 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
 {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[4]) // 8 columns
-{
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t saddr)
@@ -993,28 +1000,27 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
             }
             if (nc > 1)
                 load_kb(1);
-            // H^T Q^T into Y^T; rest: with the remainders of H
-            auto mul_qh = [&](uint32_t dy, bool rest) {
+            // H^T Q^T into Y^T
+            auto mul_qh = [&](uint32_t dy) {
                 for (int ks = 0; ks < a.nks; ++ks) {
                     const uint64_t qd = sw128_desc(s_base + Sm::kQ + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024);
                     umma_bf16_ts(dy, tmem + kDwH + 16 * ks, qd, kIdTok, ks > 0);
-                    if (rest)
-                        umma_bf16_ts(dy, tmem + kDwH + 16 * ks + 8, qd, kIdTok, 1);
+                    umma_bf16_ts(dy, tmem + kDwH + 16 * ks + 8, qd, kIdTok, 1);
                 }
                 commit(bar_qh);
             };
-            // + (w o U)^T P'^T, or U^T P'^T, in halves of another shape: after H^T Q^T has completed
-            auto mul_up = [&](uint32_t dy, bool copy) {
-                const uint32_t uh = tmem + (copy ? Sh::kUh : kDwD2), ul = tmem + (copy ? Sh::kUl : kDwD2 + 8);
+            // + (w o U)^T P'^T, in halves of another shape: after H^T Q^T has completed
+            auto mul_up = [&](uint32_t dy) {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int ks = 0; ks < 2 + 2 * hf; ++ks) {
+                        const uint32_t uh = tmem + kDwD2 + 16 * ks;
                         const uint32_t at = s_base + Sm::kP + dc_slice(ks) + (ks < 2 ? 1024 * hf : 0);
                         const uint64_t ph = sw32_desc(at), pl = sw32_desc(at + kDcMat);
-                        umma_bf16_ts(dy + 32 * hf, uh + 16 * ks, ph, kIdHalf, 1);
-                        umma_bf16_ts(dy + 32 * hf, ul + 16 * ks, ph, kIdHalf, 1);
-                        umma_bf16_ts(dy + 32 * hf, uh + 16 * ks, pl, kIdHalf, 1);
+                        umma_bf16_ts(dy + 32 * hf, uh, ph, kIdHalf, 1);
+                        umma_bf16_ts(dy + 32 * hf, uh + 8, ph, kIdHalf, 1);
+                        umma_bf16_ts(dy + 32 * hf, uh, pl, kIdHalf, 1);
                     }
                 commit(bar_y);
             };
@@ -1057,7 +1063,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_qh(dy, true);
+                    mul_qh(dy);
                 }
                 // U^T once R is written: the blocks of T on and below the diagonal
                 if (!mbar_wait(bar_b + st, ph2, status) || !mbar_wait(arr_r, ph, status)) {
@@ -1065,7 +1071,6 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                     break;
                 }
                 tc_fence_after();
-                const bool copy = reinterpret_cast<const volatile float *>(sm + Sm::kB + st * kDcHead + kDcE)[1] != 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -1100,10 +1105,9 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_qh(dy, !copy); // (the remainders' places may be taken by U)
+                    mul_qh(dy);
                 }
-                // U is written: dH^T over H, which has been read (with two CTAs a copy of U, in the
-                // place of H's remainders, too)
+                // w o U is written: dH^T over H, which has been read
                 if (!mbar_wait(arr_u, ph, status) || (outs && !mbar_wait(bar_p, ph, status))) {
                     ok = false;
                     break;
@@ -1115,12 +1119,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    mul_up(dy, copy);
-                    if (copy && !mbar_wait(bar_y, ph, status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    mul_up(dy);
                 }
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
@@ -1139,7 +1138,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 }
                 commit(bar_dh + 1);
                 if (outs && kLate)
-                    mul_up(dy, copy);
+                    mul_up(dy);
             }
             // let every load and product in flight finish before the tensor memory is freed:
             // the latest phase of each barrier
@@ -1236,27 +1235,28 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                 break;
             }
             const float2 em = *reinterpret_cast<const float2 *>(blk + kDcE); // E_63, mode
-            // ---- 2^e o Q in place, in chunks with cuts or strong decays; with two CTAs while U^T runs
-            auto scale_q = [&]() {
-                if (!wait(bar_q, ph))
-                    return false;
+            // ---- rows of K (which 0) or Q (1) scaled by powers of two in place, in chunks with cuts
+            // or strong decays
+            auto scale = [&](int from, int to) {
 #pragma unroll 1
-                for (int i = 0; i < 1024 / (32 * kWarps); ++i) {
-                    const int e = tid + 32 * kWarps * i; // 16-byte chunk: tile, token, position
-                    const float s = dc_power(ss_[(e >> 3) & 63]);
-                    uint4 *p = reinterpret_cast<uint4 *>(sm + Sm::kQ + 16 * e);
-                    const uint4 v = *p;
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        o[x] = pack_bf16x2(s * __uint_as_float(in[x] << 16), s * __uint_as_float(in[x] & 0xffff0000u));
-                    *p = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int which = from; which < to; ++which) {
+                    if (!wait(which ? bar_q : bar_k + st, which ? ph : ph2))
+                        return false;
+                    unsigned char *tiles = sm + (which ? Sm::kQ : Sm::kK + st * 16384);
+                    const unsigned char *pow = blk + kDcPow + 64 * which;
+#pragma unroll 4
+                    for (int i = 0; i < 1024 / (32 * kWarps); ++i) {
+                        const int e = 32 * (kWarps * i + warp) + ln; // 16-byte chunk: tile, token, position
+                        const uint32_t f = uint32_t(pow[(e >> 3) & 63]) * 0x00800080u; // the power as two bf16
+                        uint4 *p = reinterpret_cast<uint4 *>(tiles + 16 * e);
+                        const uint4 v = *p;
+                        *p = make_uint4(mul_bf16x2(v.x, f), mul_bf16x2(v.y, f), mul_bf16x2(v.z, f), mul_bf16x2(v.w, f));
+                    }
                 }
                 fence_proxy_async_smem();
                 return true;
             };
-            if (kLate && outs && em.y != 0.0f && !scale_q()) {
+            if (kLate && outs && em.y != 0.0f && !scale(1, 2)) {
                 ok = false;
                 break;
             }
@@ -1299,32 +1299,25 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
             tmem_st_wait();
             if (!(a.hold && c == 0))
                 arrive(arr_r);
-            if (!kLate && outs && em.y != 0.0f && !scale_q()) {
+            // (K H^T is done; all of this while U^T runs)
+            if (em.y != 0.0f && !scale(0, !kLate && outs ? 2 : 1)) {
                 ok = false;
                 break;
             }
             if (!kLate)
                 arrive(arr_q);
-            // ---- w o U over U^T, and where the outputs need it a copy of U^T ---------------------
+            // ---- w o U over U^T --------------------------------------------------------------
             if (!wait(bar_u, ph)) {
                 ok = false;
                 break;
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const uint32_t ml = lanes + (uint32_t(16 * m) << 16), at = ml + kDwD2 + kTok * cg;
+                const uint32_t at = lanes + (uint32_t(16 * m) << 16) + kDwD2 + kTok * cg;
 #pragma unroll
                 for (int j = 0; j < kTok / 16; ++j) {
                     uint32_t r[8], w[8];
                     tmem_ld_frag(at + 16 * j, r);
-                    if (outs && em.y != 0.0f) {
-                        uint32_t uh[4], ul[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dw_split2(dw_pair(r, i), uh[i], ul[i]);
-                        tmem_st_frag(ml + Sh::kUh + 16 * (kTok / 16 * cg + j), uh);
-                        tmem_st_frag(ml + Sh::kUl + 16 * (kTok / 16 * cg + j), ul);
-                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float2 wv = *reinterpret_cast<const float2 *>(sw + 16 * j + 8 * i);
@@ -1349,9 +1342,7 @@ ss_delta_walk_kernel(const __grid_constant__ DeltaWalkArgs a, const __grid_const
                                      r);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float2 sv = *reinterpret_cast<const float2 *>(ss_ + kTok * cg + 16 * j + 8 * i + tc);
-                            sv.x = em.y == 0.0f ? sv.x : dc_mantissa(sv.x);
-                            sv.y = em.y == 0.0f ? sv.y : dc_mantissa(sv.y);
+                            const float2 sv = *reinterpret_cast<const float2 *>(ss_ + kTok * cg + 16 * j + 8 * i + tc);
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float2 y = __fmul2_rn(sv, dw_pair(r, 2 * i + x));

@@ -151,6 +151,9 @@ def test_factors_of_a_chunk(decay):
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     ssscan.ss_delta_scan(**_cuda_dict(dict(inp, h0=torch.zeros(1, 1, 128, 128))), scale=1.0, workspace=ws)
     c, w, s, e = ws[2 * 6144:2 * 6144 + 4 * 256].view(F32).double().cpu().view(4, 64)
+    if e[1]:    # strong decays: w and s are kept as factors of powers of two, whose exponents' bits follow
+        power = torch.exp2(ws[2 * 6144 + 3 * 256 + 16:][:128].double().cpu().view(2, 64) - 127)
+        w, s = w * power[0], s * power[1]
     G = inp["g"].double().view(-1).cumsum(0)
     for got, log, what in ((c, G, "c"), (s, G, "s"), (w, G[-1] - G, "w"), (e[:1], G[-1:], "E_63")):
         rel = ((got - log.exp()) / log.exp()).abs()[log > -86.0]   # (below: under float32's normal range)
@@ -165,14 +168,14 @@ def test_error_of_the_chunked_form_in_norm(orc, shape, slow):
     mantissa); keeping the remainder in bfloat16 too leaves the square of it, 2.8e-6.  The
     state: five such splits on the way of a chunk (H, R, T, w o U and the product of two
     remainders that is left out), 6.2e-6 as they fall, tripled for the chunks that a state
-    remembers.  The outputs: the rounding of their own, and in chunks with a cut or strong
-    decays that of H in Q H: 1.66e-3 sqrt(2) = 2.4e-3.  A lost remainder would cost either 1e-3."""
+    remembers.  The outputs: the rounding of their own, 1.66e-3; 1.8e-3 for what a sample of a few
+    thousand may differ from it.  A lost remainder would cost either 1e-3 more."""
     inp = make_delta_inputs(*shape, "bf16", seed=3660 + sum(shape), h0=True)
     if slow:
         inp["g"] = inp["g"] * 1e-2
     y, fs = _scan(inp, scale=1.0, qk_l2norm=True)
     ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
-    for got, want, tol, what in ((y, ref["outputs"], 2.4e-3, "outputs"), (fs, ref["final_state"], 1.9e-5, "state")):
+    for got, want, tol, what in ((y, ref["outputs"], 1.8e-3, "outputs"), (fs, ref["final_state"], 1.9e-5, "state")):
         want = torch.from_numpy(want)
         err = float((got.double() - want).norm() / want.norm())
         assert err <= tol, f"{what}: {err:.2e}"
@@ -226,5 +229,5 @@ def test_keys_that_resemble_each_other(orc, heads_v, seq, decay, spread, same):
     ref = orc.delta_scan(**inp, scale=1.0, qk_l2norm=True)
     assert_close(y, ref["outputs"], TOL[BF16], "outputs")
     want = torch.from_numpy(ref["outputs"])
-    assert float((y.double() - want).norm() / want.norm()) <= 2.4e-3
+    assert float((y.double() - want).norm() / want.norm()) <= 1.8e-3
     assert_close(fs, ref["final_state"], TOL[F32], "final state")
