@@ -156,12 +156,13 @@ struct DeltaPrepArgs {
 // key head repeat its two products, a tenth of the work: kept in registers over the heads
 // they cost the occupancy that hides the rest.)
 //
-// Measured: 136 us for 8192 chunks of 128 keys (8 x 2048 tokens x 32 heads), 139 MB read and
-// 111 MB written, 1.8 TB/s: HBM does not bound it.  8300 warp instructions a chunk, issued in
-// 48% of the cycles by 19 warps an SM: instruction issue and the latencies between them.
-// Steps left out in turn: the merges of T 33 us, K K^T and Q K^T 31 us, A and P 18 us, the
-// block's store 8 us; without any of the work 32 us.
-// With T built by packed fp32 arithmetic on A in shared memory: 150 us.
+// Measured: 135 us for 8192 chunks of 128 keys (8 x 2048 tokens x 32 heads), 145 us where an
+// eighth of the heads decays strongly; 139 MB read and 157 MB written, 2.0 TB/s: HBM does not
+// bound it.  8600 warp instructions a chunk, issued in 47% of the cycles by 19 warps an SM:
+// instruction issue and the latencies between them.  With P in one part (136 us on the same
+// inputs as 145), steps left out in turn: the merges of T 33 us, K K^T and Q K^T 31 us, A and P
+// 18 us, the block's store 8 us; without any of the work 32 us; and with T built by packed fp32
+// arithmetic on A in shared memory 150 us.
 
 constexpr int kDpThreads = 128;
 constexpr int kDpRow = 136;   // elements between rows of the q and k tiles (272 bytes)
@@ -587,10 +588,11 @@ __global__ void __launch_bounds__(kDpThreads, 5) ss_delta_prep_kernel(const Delt
 // ---- the walk ------------------------------------------------------------------------
 
 // What bounds it is the chain of hand-overs from one product to the next (KH^T, R, U, dH, H),
-// chunk after chunk: without any element-wise work two walks an SM still take 89 us of the
-// 170 us that 256 walks of 32 chunks (8 x 2048 tokens x 32 heads of 128 x 128) take, the
-// tensor cores busy 32% of the time, 446 MB read and 120 MB written.  Alone on its SM a walk
-// of 32 chunks takes 98 us, 3.1 us a chunk.
+// chunk after chunk.  256 walks of 32 chunks (8 x 2048 tokens x 32 heads of 128 x 128) take
+// 169-178 us, two an SM, and 189 us where an eighth of the heads decays strongly: tensor cores
+// busy 35% of the time, instructions issued in 41% of the cycles, 497 MB read and 124 MB
+// written.  Alone on its SM a walk of 32 chunks takes 100 us, 3.1 us a chunk.  (Two walks an SM
+// without any element-wise work took 89 us of the 170 us of a walk with fewer products.)
 //
 // G: groups of four compute warps, each with a G-th of the columns: 2 (two CTAs per SM) or
 // 4 (one CTA per SM).  A CTA alone on its SM has room for Y^T beside the rest, in two places
