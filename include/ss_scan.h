@@ -419,11 +419,12 @@ SS_API int ss_gated_scan(int64_t batch, int64_t seq, int64_t dk, int64_t dv, ss_
  *    16-byte aligned tensors, strides that are multiples of 8 and a workspace: chunks of 64
  *    tokens on the tensor cores.  The state is held in float32 and computed operands in 16
  *    bits of mantissa: final_state follows float32 arithmetic to about 5e-6 of its size (to
- *    4e-5 with keys that resemble each other or beta |k|^2 past 1, to 1e-3 with both where
- *    nothing decays), and outputs are off by little more than their own rounding.  Few heads and a long sequence
- *    are cut into segments that run at once.  Columns whose state or outputs become infinite
- *    or NaN on the way (writes past about 1e20 under strong decays do, too) are walked once
- *    more token by token, 2.6 us each: right, but not fast;
+ *    1e-5 with short keys that decay slowly, to 4e-5 with keys that resemble each other or
+ *    beta |k|^2 past 1, to 1e-3 with both where nothing decays), and outputs are off by
+ *    little more than their own rounding.  Few heads and a long sequence are cut into
+ *    segments that run at once.  Columns whose state or outputs become infinite or NaN on
+ *    the way (writes past about 1e20 under strong decays do, too) are walked once more token
+ *    by token, 2.6 us each: right, but not fast;
  *  - every other case: token by token, all arithmetic in float32.  A long prompt takes
  *    many times as long (16384 tokens x 32 heads in bf16: 5.3 ms for dk = dv = 100, 0.54 ms
  *    for 104), so sizes, strides and addresses outside the first form are worth padding.
