@@ -750,10 +750,10 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, const uint32_t
 // a value reaches tokens that do not depend on it (those before it, and those behind a reset);
 // it then always stays in the state, which the walk looks at once, at its end.  Outputs are
 // looked at as they leave, since they can pass the range of fp32 on the way to finite values:
-// U^T P'^T is up to 2^60 times what it stands for.  Here a token only meets what it depends on.
-// From the state after the segment before when that is finite, or from the first token.  Two
-// syncs a token, two threads a column, the state in shared memory: 2.6 us a token (5.2 ms for
-// 2048 tokens), for inputs that hold or lead to such values only.
+// (w o U)^T P'^T is up to 2^60 times what it stands for.  Here a token only meets what it
+// depends on.  From the state after the segment before when that is finite, or from the first
+// token.  Two syncs a token, two threads a column, the state in shared memory: 2.6 us a token
+// (5.2 ms for 2048 tokens), for inputs that hold or lead to such values only.
 __device__ __noinline__ void delta_rewalk(const DeltaWalkArgs &a, unsigned char *sm, int64_t bh, int seg, int n0)
 {
     const DeltaArgs &d = a.d;

@@ -231,3 +231,26 @@ def test_keys_that_resemble_each_other(orc, heads_v, seq, decay, spread, same):
     want = torch.from_numpy(ref["outputs"])
     assert float((y.double() - want).norm() / want.norm()) <= 1.8e-3
     assert_close(fs, ref["final_state"], TOL[F32], "final state")
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 1, 200, 128, 128), (3, 2400, 1, 60, 64, 64)])
+@pytest.mark.parametrize("resets", [None, 40])
+def test_timed_out_waits_with_two_walks_an_sm(shape, resets):
+    """An arrival of every walk's first chunk withheld, under a limit of 2 ms: the waits give
+    up, the status says so, and the next call gives the normal answer."""
+    d = _cuda_dict(make_delta_inputs(*shape, "bf16", seed=3690, h0=True, reset_mean_doc=resets))
+    ref = ssscan.ss_delta_scan(**d, qk_l2norm=True)
+    assert ssscan.ss_debug_status() == "SS_OK"
+    ssscan.ss_debug_set_wait_limit(2000)
+    ssscan.ss_debug_set_gated_path(3)
+    try:
+        ssscan.ss_delta_scan(**d, qk_l2norm=True)
+        torch.cuda.synchronize()
+        assert ssscan.ss_debug_status() == "SS_ERR_TIMEOUT"
+    finally:
+        ssscan.ss_debug_set_gated_path(0)
+        ssscan.ss_debug_set_wait_limit(0)
+    out = ssscan.ss_delta_scan(**d, qk_l2norm=True)
+    torch.cuda.synchronize()
+    assert ssscan.ss_debug_status() == "SS_OK"
+    assert torch.equal(out["outputs"], ref["outputs"]) and torch.equal(out["final_state"], ref["final_state"])
